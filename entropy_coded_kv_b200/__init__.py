@@ -18,6 +18,8 @@ import torch
 
 from . import _lib
 from ._lib import EccoError, Desc, Segment, STATS_FIELDS
+from .paged import (OutOfPages, PageAllocator, PagedCache, compact_pages, copy_pages, paged_append, paged_attention,
+                    paged_attention_workspace_bytes, rope, rope_frequencies, rope_table)
 
 GROUP = 128
 GROUP_ACT = 64  # activation format: 64 values per 64-byte block
@@ -28,7 +30,10 @@ __all__ = ["Tables", "encode", "decode", "decode_gemv", "decode_multi", "encode_
            "decode_attention", "attention_workspace_bytes", "decode_attention_static",
            "decode_attention_staged", "attention_staged_workspace_bytes",
            "encode_act", "decode_act", "GROUP_ACT", "learn_tables", "huffman_lengths",
-           "new_stats", "read_stats", "flat_desc", "kv_append_desc", "EccoError", "Desc"]
+           "new_stats", "read_stats", "flat_desc", "kv_append_desc", "EccoError", "Desc",
+           "rope", "rope_table", "rope_frequencies", "paged_append", "paged_attention",
+           "paged_attention_workspace_bytes", "copy_pages", "compact_pages", "PagedCache", "PageAllocator",
+           "OutOfPages"]
 
 
 class Tables:

@@ -20,6 +20,9 @@ ECCO_ERR_TIMEOUT = -8
 ATTENTION_STATIC_WS_BYTES = 4 << 20
 SELECT_MINMAX = 0
 SELECT_MSE = 1
+BF16, F16, F32 = 0, 1, 2
+ROPE_INTERLEAVED, ROPE_INVERSE = 1, 2
+MAX_BATCH = 1024
 TABLES_BYTES = 7952
 MAX_SEGMENTS = 256
 
@@ -30,7 +33,8 @@ EXPORTED = [
     "ecco_decode_attention_workspace_bytes", "ecco_decode_attention_static", "ecco_select_encode_ex",
     "ecco_select_encode_act", "ecco_decode_act", "ecco_learn_tables", "ecco_huffman_lengths",
     "ecco_decode_attention_staged", "ecco_decode_attention_staged_workspace_bytes",
-    "ecco_selftest_wait_timeout",
+    "ecco_selftest_wait_timeout", "ecco_rope_table", "ecco_rope", "ecco_paged_append", "ecco_paged_attention",
+    "ecco_paged_attention_workspace_bytes", "ecco_copy_pages", "ecco_compact_pages",
 ]
 
 
@@ -42,6 +46,12 @@ class Desc(ctypes.Structure):
 class Segment(ctypes.Structure):
     _fields_ = [("tables", ctypes.c_void_p), ("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
                 ("desc", Desc)]
+
+
+class Paged(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("table_stride", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("cu_q", ctypes.c_void_p)]
 
 
 STATS_FIELDS = ["n_groups", "n_zero", "n_clipped", "n_padded", "n_records", "n_nonfinite",
@@ -89,7 +99,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                         ctypes.c_size_t, P]
     L.ecco_decode_attention_staged_workspace_bytes.argtypes = [I, I, I, I]
     L.ecco_decode_attention_staged.argtypes = L.ecco_decode_attention.argtypes
-    sizes = ("ecco_decode_attention_workspace_bytes", "ecco_decode_attention_staged_workspace_bytes")
+    F = ctypes.c_float
+    L.ecco_rope_table.argtypes = [P, I, ctypes.c_double, I64, P, P]
+    L.ecco_rope.argtypes = [P, I64, I64, P, I64, I64, I, I64, I, I, P, I64, I, P, I, P]
+    L.ecco_paged_append.argtypes = [P, P, Paged, P, I64, I64, P, I64, I64, I64, P, P, P, I64, I, P, I, P, P]
+    L.ecco_paged_attention_workspace_bytes.argtypes = [I, I, I, I, I]
+    L.ecco_paged_attention.argtypes = [P, P, Paged, P, P, P, I64, I64, I, I64, I, I, I, F, P, I64, I64, P, P,
+                                       ctypes.c_size_t, P]
+    L.ecco_copy_pages.argtypes = [P, P, I64, I64, P, P, I64, P]
+    L.ecco_compact_pages.argtypes = [Paged, P, P, P, I64, P, I64, I, P, P]
+    sizes = ("ecco_decode_attention_workspace_bytes", "ecco_decode_attention_staged_workspace_bytes",
+             "ecco_paged_attention_workspace_bytes")
     for fn in EXPORTED:
         if fn != "ecco_strerror" and fn not in sizes:
             getattr(L, fn).restype = I

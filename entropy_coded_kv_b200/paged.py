@@ -1,0 +1,583 @@
+"""Paged compressed KV cache: rotary positions, append, attention of new tokens,
+page copies and compaction (include/ecco.h, "Paged compressed cache").
+
+A pool holds the 64-byte blocks of one layer's keys (or values) in pages,
+uint8 [n_pages, kv_heads, page_size, 64]; a sequence is a row of page numbers
+and a length.  The functions below are the thin binding: they check shapes,
+types and devices and pass device pointers and the current stream on.
+`PageAllocator` keeps the book of pages on the host, and `PagedCache` joins it
+with the pools and the calls."""
+from __future__ import annotations
+
+import ctypes
+import heapq
+import math
+
+import torch
+
+from . import _lib
+
+GROUP, BLOCK_BYTES = 128, 64
+_DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16, torch.float32: _lib.F32}
+
+
+def _on(t, dtype, dim, name, device=None):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name} is on {t.device}" + (f", expected {device}" if device is not None else ""))
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions")
+    return t.device
+
+
+def _contiguous(t, name):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _strides(t, name):
+    """Token and head strides of [tokens, heads, dim]; those of a dimension of size one say nothing."""
+    n, h, d = t.shape
+    if d > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    sh = t.stride(1) if h > 1 else (d + 7) // 8 * 8
+    return (t.stride(0) if n > 1 else h * sh), sh
+
+
+def _call(fn, device, *args):
+    """The library call on `device`'s current stream, with that device current."""
+    f = getattr(_lib.load(), fn)
+    if torch.cuda.current_device() == device.index:
+        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc:
+        _lib.check(rc, fn)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+# ------------------------------------------------------------------ rotary positions
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None):
+    """(inv_freq, magnitude): angle of pair i per position, base ** (-2 i /
+    rotary_dim), and the factor on cos and sin.  `scaling` stretches them for
+    long contexts by its "factor" s, by "kind":
+      "linear"  every frequency / s;
+      "ntk"     base * s ** (rotary_dim / (rotary_dim - 2)): the slowest pair is
+                stretched by s, the fastest hardly;
+      "bands"   pairs that turn fewer than `low` times (1) over the `original`
+                context are stretched by s, those above `high` (4) are kept, and
+                between them the two are mixed linearly in the number of turns;
+      "yarn"    the same with a ramp linear in the pair's index between the
+                pairs that turn `high` (32) and `low` (1) times, and cos and sin
+                times 0.1 ln s + 1 (arXiv 2309.00071)."""
+    half = rotary_dim // 2
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    if not base > 1 or not math.isfinite(base):
+        raise ValueError("base must be above 1")
+    freq = [base ** (-2.0 * i / rotary_dim) for i in range(half)]
+    if scaling is None:
+        return freq, 1.0
+    kind, s = scaling["kind"], float(scaling["factor"])
+    if not s >= 1 or not math.isfinite(s):
+        raise ValueError("factor must be at least 1")
+    if kind == "linear":
+        return [f / s for f in freq], 1.0
+    if kind == "ntk":
+        if rotary_dim == 2:
+            return freq, 1.0
+        return rope_frequencies(rotary_dim, base * s ** (rotary_dim / (rotary_dim - 2.0)))
+    if kind not in ("bands", "yarn"):
+        raise ValueError(f"unknown scaling kind {kind!r}")
+    original = float(scaling["original"])
+    low, high = float(scaling.get("low", 1)), float(scaling.get("high", 4 if kind == "bands" else 32))
+    if not (original > 0 and 0 < low < high):
+        raise ValueError("scaling wants original > 0 and 0 < low < high")
+    if kind == "bands":
+        keep = [min(1.0, max(0.0, (original * f / (2 * math.pi) - low) / (high - low))) for f in freq]
+        return [f * k + f / s * (1 - k) for f, k in zip(freq, keep)], 1.0
+    at = [rotary_dim * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base)) for turns in (high, low)]
+    first, last = max(0, math.floor(at[0])), min(rotary_dim - 1, math.ceil(at[1]))
+    width = max(last - first, 1e-3)
+    keep = [1 - min(1.0, max(0.0, (i - first) / width)) for i in range(half)]
+    return [f * k + f / s * (1 - k) for f, k in zip(freq, keep)], (0.1 * math.log(s) + 1.0 if s > 1 else 1.0)
+
+
+def rope_table(n_positions: int, rotary_dim: int, base: float = 10000.0, scaling: dict | None = None,
+               device=None) -> torch.Tensor:
+    """fp32 [n_positions, rotary_dim / 2, 2]: cos and sin of every position's
+    angles, from fp64 angles (rope_frequencies gives the arguments)."""
+    freq, magnitude = rope_frequencies(rotary_dim, base, scaling)
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError("the table lives on a CUDA device")
+    table = torch.empty((int(n_positions), rotary_dim // 2, 2), dtype=torch.float32, device=dev)
+    arr = (ctypes.c_double * len(freq))(*freq)
+    _call("ecco_rope_table", table.device, arr, len(freq), magnitude, int(n_positions), table.data_ptr())
+    return table
+
+
+def _table(rope, device):
+    _on(rope, torch.float32, 3, "table", device)
+    if rope.shape[2] != 2:
+        raise ValueError("table must be [n_positions, rotary_dim / 2, 2]")
+    _contiguous(rope, "table")
+    return rope.shape[0], 2 * rope.shape[1]
+
+
+def _flags(interleaved, inverse):
+    return (_lib.ROPE_INTERLEAVED if interleaved else 0) | (_lib.ROPE_INVERSE if inverse else 0)
+
+
+def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, interleaved: bool = False,
+         inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """x [tokens, heads, dim] (bf16, fp16 or fp32) with the first rotary_dim
+    values of each head turned by the angles of its row's position (int32
+    [tokens]): pairs (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if interleaved.
+    inverse turns back, which is also the gradient of x from that of the
+    result.  `out` may be x."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
+        raise TypeError("x must be a bf16, fp16 or fp32 tensor")
+    dev = _on(x, x.dtype, 3, "x")
+    n, rotary = _table(table, dev)
+    _on(positions, torch.int32, 1, "positions", dev)
+    _contiguous(positions, "positions")
+    if positions.shape[0] != x.shape[0]:
+        raise ValueError("positions must have an entry for each row of x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        _on(out, x.dtype, 3, "out", dev)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+    tokens, heads, dim = x.shape
+    _call("ecco_rope", dev, x.data_ptr(), *_strides(x, "x"), out.data_ptr(), *_strides(out, "out"), _DTYPES[x.dtype],
+          tokens, heads, dim, table.data_ptr(), n, rotary, positions.data_ptr(), _flags(interleaved, inverse))
+    return out
+
+
+# ------------------------------------------------------------------ the paged cache
+def _paged(k_pages, v_pages, page_table, kv_lens, cu_q, device):
+    _on(k_pages, torch.uint8, 4, "k_pages", device)
+    _on(v_pages, torch.uint8, 4, "v_pages", device)
+    _on(page_table, torch.int32, 2, "page_table", device)
+    _on(kv_lens, torch.int32, 1, "kv_lens", device)
+    if k_pages.shape != v_pages.shape or k_pages.shape[3] != BLOCK_BYTES:
+        raise ValueError("k_pages / v_pages must be [n_pages, kv_heads, page_size, 64] of the same shape")
+    _contiguous(k_pages, "k_pages")
+    _contiguous(v_pages, "v_pages")
+    _contiguous(kv_lens, "kv_lens")
+    batch, max_pages = page_table.shape
+    if max_pages > 1 and page_table.stride(1) != 1:
+        raise ValueError("the entries of a page_table row must be contiguous")
+    if kv_lens.shape[0] != batch:
+        raise ValueError("kv_lens must have an entry for each row of page_table")
+    if cu_q is not None:
+        _on(cu_q, torch.int32, 1, "cu_q", device)
+        _contiguous(cu_q, "cu_q")
+        if cu_q.shape[0] != batch + 1:
+            raise ValueError("cu_q must have one entry more than page_table has rows")
+    n_pages, heads, page_size, _ = k_pages.shape
+    return _lib.Paged(n_pages, page_size, heads, batch, max_pages, page_table.stride(0) if batch > 1 else max_pages,
+                      page_table.data_ptr(), kv_lens.data_ptr(), _ptr(cu_q))
+
+
+def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_tables, v_tables,
+                 page_table: torch.Tensor, kv_lens: torch.Tensor, cu_q: torch.Tensor,
+                 rope: torch.Tensor | None = None, positions: torch.Tensor | None = None, interleaved: bool = False,
+                 inverse: bool = False, stats: torch.Tensor | None = None) -> None:
+    """Encodes the new tokens' keys and values (bf16 [tokens, kv_heads, 128])
+    into their pages: row cu_q[b] + i goes to position kv_lens[b] - (cu_q[b + 1]
+    - cu_q[b]) + i of sequence b (kv_lens counts the new tokens).  With `rope`
+    (a rope_table of at most 128 values) the keys are turned first, by their own
+    positions or by `positions` (int32 [tokens])."""
+    dev = k_tables.device
+    _on(k, torch.bfloat16, 3, "k", dev)
+    _on(v, torch.bfloat16, 3, "v", dev)
+    p = _paged(k_pages, v_pages, page_table, kv_lens, cu_q, dev)
+    if k.shape != v.shape or k.shape[1] != p.kv_heads or k.shape[2] != GROUP:
+        raise ValueError("k and v must be [tokens, kv_heads, 128]")
+    n, rotary = (0, 0) if rope is None else _table(rope, dev)
+    if positions is not None:
+        _on(positions, torch.int32, 1, "positions", dev)
+        _contiguous(positions, "positions")
+        if positions.shape[0] != k.shape[0]:
+            raise ValueError("positions must have an entry for each row of k")
+    if stats is not None:
+        _on(stats, torch.int64, 1, "stats", dev)
+        if stats.numel() < len(_lib.STATS_FIELDS) or not stats.is_contiguous():
+            raise ValueError("stats must be a buffer of new_stats")
+    _call("ecco_paged_append", dev, k_tables.handle, v_tables.handle, p, k.data_ptr(), *_strides(k, "k"), v.data_ptr(),
+          *_strides(v, "v"), k.shape[0], k_pages.data_ptr(), v_pages.data_ptr(), _ptr(rope), n, rotary,
+          _ptr(positions), _flags(interleaved, inverse), _ptr(stats))
+
+
+def paged_attention_workspace_bytes(batch: int, kv_heads: int, group: int, max_q: int, max_kv: int) -> int:
+    return int(_lib.load().ecco_paged_attention_workspace_bytes(batch, kv_heads, group, max_q, max_kv))
+
+
+def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_tables, v_tables,
+                    page_table: torch.Tensor, kv_lens: torch.Tensor, cu_q: torch.Tensor, scale: float,
+                    max_q: int | None = None, max_kv: int | None = None, window: int = 0,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Causal attention of new tokens, already appended, over the paged cache.
+
+    q: bf16 [tokens, kv_heads * group, 128], rows cu_q[b] .. cu_q[b + 1] - 1 the
+    last tokens of sequence b.  Returns bf16 of q's shape; `lse` (fp32 [tokens,
+    kv_heads * group]) takes the log-sums of the scores.  window > 0: a token
+    sees the last `window` keys up to its own.  max_q and max_kv bound the new
+    tokens and the keys of one sequence (by default all rows, and what a
+    page_table row holds); they size the workspace
+    (paged_attention_workspace_bytes), which may be passed to reuse it."""
+    dev = k_tables.device
+    _on(q, torch.bfloat16, 3, "q", dev)
+    p = _paged(k_pages, v_pages, page_table, kv_lens, cu_q, dev)
+    tokens, heads, dim = q.shape
+    if dim != GROUP or heads % p.kv_heads:
+        raise ValueError("q must be [tokens, kv_heads * group, 128]")
+    group = heads // p.kv_heads
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
+    else:
+        _on(out, torch.bfloat16, 3, "out", dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is not None:
+        _on(lse, torch.float32, 2, "lse", dev)
+        _contiguous(lse, "lse")
+        if lse.shape != (tokens, heads):
+            raise ValueError("lse must be [tokens, kv_heads * group]")
+    max_q = tokens if max_q is None else int(max_q)
+    max_kv = p.max_pages * p.page_size if max_kv is None else int(max_kv)
+    if workspace is None:
+        workspace = torch.empty(max(1, paged_attention_workspace_bytes(p.batch, p.kv_heads, group, max_q, max_kv)),
+                                dtype=torch.uint8, device=dev)
+    else:
+        _on(workspace, torch.uint8, 1, "workspace", dev)
+        _contiguous(workspace, "workspace")
+    _call("ecco_paged_attention", dev, k_tables.handle, v_tables.handle, p, k_pages.data_ptr(), v_pages.data_ptr(),
+          q.data_ptr(), *_strides(q, "q"), group, tokens, max_q, max_kv, int(window), float(scale), out.data_ptr(),
+          *_strides(out, "out"), _ptr(lse), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def _host_ids(ids, name):
+    t = torch.as_tensor(ids, dtype=torch.int32) if not isinstance(ids, torch.Tensor) else ids
+    if t.dtype != torch.int32 or t.device.type != "cpu" or t.dim() != 1:
+        raise TypeError(f"{name} must be a list or a one-dimensional int32 CPU tensor")
+    return t.contiguous()
+
+
+def copy_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, src, dst) -> None:
+    """Copies page src[i] to page dst[i] of both pools.  src and dst are page
+    numbers on the host (lists or int32 CPU tensors); no destination may appear
+    twice or be a source."""
+    dev = _on(k_pages, torch.uint8, 4, "k_pages")
+    _on(v_pages, torch.uint8, 4, "v_pages", dev)
+    if k_pages.shape != v_pages.shape or k_pages.shape[3] != BLOCK_BYTES:
+        raise ValueError("k_pages / v_pages must be [n_pages, kv_heads, page_size, 64] of the same shape")
+    _contiguous(k_pages, "k_pages")
+    _contiguous(v_pages, "v_pages")
+    src, dst = _host_ids(src, "src"), _host_ids(dst, "dst")
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must be of the same length")
+    n_pages, heads, page_size, _ = k_pages.shape
+    _call("ecco_copy_pages", dev, k_pages.data_ptr(), v_pages.data_ptr(), n_pages, heads * page_size * BLOCK_BYTES,
+          src.data_ptr(), dst.data_ptr(), src.numel())
+
+
+def compact_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                  keep: torch.Tensor, dst_table: torch.Tensor, out_lens: torch.Tensor | None = None) -> torch.Tensor:
+    """Moves the kept tokens of each sequence (keep: bool or uint8 [batch, at
+    least the longest length]) to the front of the pages dst_table (int32
+    [batch, dst_pages]), in their order, and returns the new lengths (int32
+    [batch]).  The blocks move as they are: nothing is encoded again.  The
+    destination pages may not be among the pages read."""
+    dev = _on(k_pages, torch.uint8, 4, "k_pages")
+    p = _paged(k_pages, v_pages, page_table, kv_lens, None, dev)
+    _on(keep, keep.dtype if isinstance(keep, torch.Tensor) and keep.dtype in (torch.bool, torch.uint8) else torch.bool,
+        2, "keep", dev)
+    _contiguous(keep, "keep")
+    _on(dst_table, torch.int32, 2, "dst_table", dev)
+    if dst_table.shape[1] > 1 and dst_table.stride(1) != 1:
+        raise ValueError("the entries of a dst_table row must be contiguous")
+    if keep.shape[0] != p.batch or dst_table.shape[0] != p.batch:
+        raise ValueError("keep and dst_table must have a row for each of page_table")
+    if out_lens is None:
+        out_lens = torch.empty(p.batch, dtype=torch.int32, device=dev)
+    _on(out_lens, torch.int32, 1, "out_lens", dev)
+    _contiguous(out_lens, "out_lens")
+    if out_lens.shape[0] != p.batch:
+        raise ValueError("out_lens must have an entry for each row of page_table")
+    _call("ecco_compact_pages", dev, p, k_pages.data_ptr(), v_pages.data_ptr(), keep.data_ptr(), keep.shape[1],
+          dst_table.data_ptr(), dst_table.stride(0) if p.batch > 1 else dst_table.shape[1], dst_table.shape[1],
+          out_lens.data_ptr())
+    return out_lens
+
+
+# ------------------------------------------------------------------ the book of pages
+class OutOfPages(RuntimeError):
+    """The pool has fewer free pages than a request needs; nothing was changed."""
+
+
+class PageAllocator:
+    """Host-side book of a pool's pages: which sequence holds which pages, how
+    many sequences share a page, which are free.  Sequences are numbered; the
+    lowest free page is handed out first.  A shared page is never written: the
+    partly filled last page of a forked sequence is copied when it grows."""
+
+    def __init__(self, n_pages: int, page_size: int):
+        if n_pages < 0 or page_size < 1:
+            raise ValueError("n_pages >= 0 and page_size >= 1")
+        self.n_pages, self.page_size = int(n_pages), int(page_size)
+        self._free = list(range(self.n_pages))
+        self._users = [0] * self.n_pages
+        self._pages: dict[int, list[int]] = {}
+        self._len: dict[int, int] = {}
+        self._next = 0
+
+    @property
+    def free_pages(self) -> int:
+        return len(self._free)
+
+    def pages(self, seq: int) -> list[int]:
+        return list(self._pages[seq])
+
+    def length(self, seq: int) -> int:
+        return self._len[seq]
+
+    def _take(self) -> int:
+        p = heapq.heappop(self._free)
+        self._users[p] = 1
+        return p
+
+    def _drop(self, page: int) -> None:
+        self._users[page] -= 1
+        if self._users[page] == 0:
+            heapq.heappush(self._free, page)
+
+    def add(self) -> int:
+        """A new, empty sequence."""
+        s = self._next
+        self._next += 1
+        self._pages[s], self._len[s] = [], 0
+        return s
+
+    def fork(self, seq: int) -> int:
+        """A sequence with the same tokens, on the same pages."""
+        pages, n = self._pages[seq], self._len[seq]
+        s = self.add()
+        for p in pages:
+            self._users[p] += 1
+        self._pages[s], self._len[s] = list(pages), n
+        return s
+
+    def free(self, seq: int) -> None:
+        for p in self._pages.pop(seq):
+            self._drop(p)
+        del self._len[seq]
+
+    def extend(self, seqs: list[int], new: list[int]) -> list[tuple[int, int]]:
+        """Room for new[i] more tokens of each sequence.  Returns the (source,
+        destination) pages to copy before they are written."""
+        if len(seqs) != len(new) or len(set(seqs)) != len(seqs):
+            raise ValueError("one count for each sequence, and no sequence twice")
+        if any(n < 0 for n in new):
+            raise ValueError("counts must not be negative")
+        ps = self.page_size
+        # users: the sharers left once the earlier sequences of this call have their own copy
+        shared, need, split = {}, 0, []
+        for s, n in zip(seqs, new):
+            pages, have = self._pages[s], self._len[s]
+            need += max(0, -(-(have + n) // ps) - len(pages))
+            if n and have % ps:
+                last = pages[have // ps]
+                if shared.setdefault(last, self._users[last]) > 1:
+                    shared[last] -= 1
+                    need += 1
+                    split.append(s)
+        if need > len(self._free):
+            raise OutOfPages(f"{need} pages needed, {len(self._free)} free")
+        copies = []
+        for s in split:
+            at = self._len[s] // ps
+            old, own = self._pages[s][at], self._take()
+            self._pages[s][at] = own
+            self._drop(old)
+            copies.append((old, own))
+        for s, n in zip(seqs, new):
+            self._len[s] += n
+            while len(self._pages[s]) * ps < self._len[s]:
+                self._pages[s].append(self._take())
+        return copies
+
+    def shrink(self, seq: int, length: int) -> None:
+        """Drops the tokens from `length` on, and the pages that only they used."""
+        if not 0 <= length <= self._len[seq]:
+            raise ValueError("length must be between 0 and the sequence's")
+        keep = -(-length // self.page_size)
+        for p in self._pages[seq][keep:]:
+            self._drop(p)
+        del self._pages[seq][keep:]
+        self._len[seq] = length
+
+    def replace(self, seqs: list[int]) -> list[list[int]]:
+        """As many fresh pages as each sequence has; the caller moves the tokens
+        to them and then calls `settle`, or gives them back with `cancel`."""
+        need = sum(len(self._pages[s]) for s in seqs)
+        if len(set(seqs)) != len(seqs):
+            raise ValueError("no sequence twice")
+        if need > len(self._free):
+            raise OutOfPages(f"{need} pages needed, {len(self._free)} free")
+        return [[self._take() for _ in self._pages[s]] for s in seqs]
+
+    def settle(self, seqs: list[int], fresh: list[list[int]], lengths: list[int]) -> None:
+        for s, pages, n in zip(seqs, fresh, lengths):
+            for p in self._pages[s]:
+                self._drop(p)
+            self._pages[s] = pages
+            self._len[s] = len(pages) * self.page_size
+            self.shrink(s, n)
+
+    def cancel(self, fresh: list[list[int]]) -> None:
+        for pages in fresh:
+            for p in pages:
+                self._drop(p)
+
+
+class Step:
+    """One batch's view of the cache, on the device: page_table, kv_lens (the
+    new tokens among them), cu_q, and the bounds max_q and max_kv."""
+
+    def __init__(self, page_table, kv_lens, cu_q, positions, tokens, max_q, max_kv):
+        self.page_table, self.kv_lens, self.cu_q, self.positions = page_table, kv_lens, cu_q, positions
+        self.tokens, self.max_q, self.max_kv = tokens, max_q, max_kv
+
+
+class PagedCache:
+    """A paged compressed cache of several layers: pools, allocator and calls.
+
+        cache = PagedCache(n_pages, page_size, kv_heads, k_tables, v_tables)   # one pair of tables a layer
+        s = cache.add()
+        step = cache.extend([s], [len(prompt)])          # pages, lengths and positions of the new tokens
+        for layer in range(cache.layers):
+            cache.append(step, layer, k, v, rope=table)  # keys turned, keys and values encoded
+            out = cache.attend(step, layer, q, scale)    # q turned by rope(q, table, step.positions)
+        t = cache.fork(s)                                # shares the pages
+        cache.compact([s], keep)                         # drops tokens
+        cache.free(t)
+
+    All calls of a cache belong on one stream: a freed page is handed out again
+    at once, and only the stream's order keeps its readers before its writers.
+    Dropped tokens leave the others' turned keys as they are, so after `compact`
+    a sequence's next position is no longer its length: `extend` continues from
+    the last position given."""
+
+    def __init__(self, n_pages: int, page_size: int, kv_heads: int, k_tables, v_tables):
+        self.k_tables = list(k_tables) if isinstance(k_tables, (list, tuple)) else [k_tables]
+        self.v_tables = list(v_tables) if isinstance(v_tables, (list, tuple)) else [v_tables]
+        if not self.k_tables or len(self.k_tables) != len(self.v_tables):
+            raise ValueError("one pair of tables for each layer")
+        self.device = self.k_tables[0].device
+        if any(t.device != self.device for t in self.k_tables + self.v_tables):
+            raise ValueError("all tables must be on one device")
+        self.layers, self.kv_heads, self.page_size = len(self.k_tables), int(kv_heads), int(page_size)
+        self.book = PageAllocator(n_pages, page_size)
+        shape = (self.layers, n_pages, kv_heads, page_size, BLOCK_BYTES)
+        self.k_pages = torch.empty(shape, dtype=torch.uint8, device=self.device)
+        self.v_pages = torch.empty(shape, dtype=torch.uint8, device=self.device)
+        self._position: dict[int, int] = {}
+
+    def _ints(self, v):
+        return torch.tensor(v, dtype=torch.int32).to(self.device)
+
+    def _table_of(self, lists):
+        width = max((len(p) for p in lists), default=0)
+        return self._ints([p + [-1] * (width - len(p)) for p in lists]).view(len(lists), width)
+
+    def add(self) -> int:
+        s = self.book.add()
+        self._position[s] = 0
+        return s
+
+    def fork(self, seq: int) -> int:
+        s = self.book.fork(seq)
+        self._position[s] = self._position[seq]
+        return s
+
+    def free(self, seq: int) -> None:
+        self.book.free(seq)
+        del self._position[seq]
+
+    def length(self, seq: int) -> int:
+        return self.book.length(seq)
+
+    def extend(self, seqs: list[int], new: list[int]) -> Step:
+        """Pages for new[i] more tokens of each sequence (OutOfPages if there are
+        too few, with nothing changed), and the batch's view for the layers'
+        calls.  Pages that are shared and about to be written are copied."""
+        copies = self.book.extend(seqs, new)
+        if copies:
+            n = self.book.n_pages
+            src = [a + l * n for l in range(self.layers) for a, _ in copies]
+            dst = [b + l * n for l in range(self.layers) for _, b in copies]
+            copy_pages(self.k_pages.flatten(0, 1), self.v_pages.flatten(0, 1), src, dst)
+        first = [self._position[s] for s in seqs]
+        for s, n in zip(seqs, new):
+            self._position[s] += n
+        lens, cu = [self.book.length(s) for s in seqs], [0]
+        for n in new:
+            cu.append(cu[-1] + n)
+        positions = [p + i for p, n in zip(first, new) for i in range(n)]
+        return Step(self._table_of([self.book.pages(s) for s in seqs]), self._ints(lens), self._ints(cu),
+                    self._ints(positions), cu[-1], max(new, default=0), max(lens, default=0))
+
+    def append(self, step: Step, layer: int, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor | None = None,
+               interleaved: bool = False, stats: torch.Tensor | None = None) -> None:
+        """Encodes the step's keys and values (bf16 [tokens, kv_heads, 128]) into the layer's pages."""
+        if k.shape[0] != step.tokens:
+            raise ValueError("k and v must have a row for each new token of the step")
+        paged_append(k, v, self.k_pages[layer], self.v_pages[layer], self.k_tables[layer], self.v_tables[layer],
+                     step.page_table, step.kv_lens, step.cu_q, rope=rope,
+                     positions=step.positions if rope is not None else None, interleaved=interleaved, stats=stats)
+
+    def attend(self, step: Step, layer: int, q: torch.Tensor, scale: float, window: int = 0,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+        """Attention of the step's tokens (bf16 [tokens, kv_heads * group, 128]) over the layer's pages."""
+        if q.shape[0] != step.tokens:
+            raise ValueError("q must have a row for each new token of the step")
+        return paged_attention(q, self.k_pages[layer], self.v_pages[layer], self.k_tables[layer],
+                               self.v_tables[layer], step.page_table, step.kv_lens, step.cu_q, scale,
+                               max_q=step.max_q, max_kv=step.max_kv, window=window, out=out, lse=lse,
+                               workspace=workspace)
+
+    def compact(self, seqs: list[int], keep: torch.Tensor) -> list[int]:
+        """Keeps the tokens of each sequence whose entry of `keep` (bool or uint8
+        [len(seqs), at least the longest length]) is not zero, in every layer,
+        and frees the pages that are left over.  Takes as many free pages as the
+        sequences hold while it runs.  Blocks until the new lengths are known;
+        returns them."""
+        lens = [self.book.length(s) for s in seqs]
+        if keep.dim() != 2 or keep.shape[0] != len(seqs) or keep.shape[1] < max(lens, default=0):
+            raise ValueError("keep must be [len(seqs), at least the longest length]")
+        if not seqs:
+            return []
+        fresh = self.book.replace(seqs)
+        try:
+            table, dst = self._table_of([self.book.pages(s) for s in seqs]), self._table_of(fresh)
+            kv_lens = self._ints(lens)
+            for layer in range(self.layers):
+                new = compact_pages(self.k_pages[layer], self.v_pages[layer], table, kv_lens, keep, dst)
+            lengths = new.tolist()
+        except BaseException:
+            self.book.cancel(fresh)
+            raise
+        self.book.settle(seqs, fresh, lengths)
+        return lengths

@@ -285,6 +285,142 @@ int ecco_decode_attention_static(const ecco_tables* k_tables, const ecco_tables*
                                  int batch, int kv_heads, int group, int seq_len, const uint16_t* q_bf16,
                                  float scale, float* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged compressed cache.  A pool of pages holds the blocks of one layer's K
+ * (or V): page P, KV head h, slot i at block index (P * kv_heads + h) *
+ * page_size + i.  A sequence is a row of page numbers and a length; token t
+ * of sequence b lies in page page_table[b][t / page_size], slot t % page_size.
+ * K and V have a pool each, of the same shape, and share the page numbers.
+ *
+ * The calls below read page_table, kv_lens and cu_q on the device, so they may
+ * change between replays of a captured graph.  What they say is checked there:
+ * an entry that names no page of the pool (or a position past the row's
+ * max_pages pages) is never dereferenced, and a length outside its bounds is
+ * clamped to them. */
+typedef struct {
+    int64_t n_pages;           /* pages of each pool */
+    int32_t page_size;         /* tokens of a page, 1..65536 */
+    int32_t kv_heads;          /* 1..1024 */
+    int32_t batch;             /* sequences, 0..ECCO_MAX_BATCH */
+    int32_t max_pages;         /* entries of a page_table row, >= 0; a row holds at most 2^30 tokens */
+    int64_t table_stride;      /* from one page_table row to the next, in entries */
+    const int32_t* page_table; /* [batch][max_pages], device */
+    const int32_t* kv_lens;    /* [batch], device: tokens of each sequence, the new ones among them */
+    const int32_t* cu_q;       /* [batch + 1], device: the new tokens of sequence b are rows cu_q[b] ..
+                                  cu_q[b + 1] - 1 of the token arrays, non-decreasing, cu_q[0] >= 0 */
+} ecco_paged;
+#define ECCO_MAX_BATCH 1024
+
+/* Rotary positions.  ecco_rope_table fills table[p][i] = (cos, sin) of the
+ * angle p * inv_freq[i] (computed in fp64, times `magnitude`, rounded once to
+ * fp32) for 0 <= p < n_positions, 0 <= i < n_freq: the scalings for long
+ * contexts are choices of inv_freq and magnitude.  inv_freq is host memory,
+ * read before the call returns; 1 <= n_freq <= 512; table 8-byte aligned
+ * device memory, [n_positions][n_freq][2] fp32. */
+int ecco_rope_table(const double* inv_freq, int n_freq, double magnitude, int64_t n_positions, float* table,
+                    void* stream);
+
+/* y = x with the first rotary_dim values of every head turned by the angles of
+ * the row's position: pairs (a, b) become
+ *   (a cos - b sin,  b cos + a sin),
+ * every product and sum one fp32 rounding, the result rounded once to the
+ * type.  The pairs are values (i, i + rotary_dim / 2), or with
+ * ECCO_ROPE_INTERLEAVED (2 i, 2 i + 1); ECCO_ROPE_INVERSE turns back (-sin):
+ * the transpose of the turn, so also the gradient of x from that of y.
+ *   x, y       [tokens][heads][dim]; token and head strides in elements, the
+ *              values of a head contiguous; y may be x itself (same strides),
+ *              otherwise they may not overlap;
+ *   dtype      ECCO_BF16, ECCO_F16 or ECCO_F32;
+ *   positions  [tokens] int32, device; one outside [0, n_positions) uses the
+ *              nearest row of the table;
+ *   table      [n_positions][rotary_dim / 2][2] fp32 (ecco_rope_table).
+ * dim % 8 == 0, 8 <= dim <= 1024; rotary_dim % 16 == 0, 16 <= rotary_dim <=
+ * dim; heads 1..65535; x, y and their strides multiples of 16 bytes; table
+ * 16-byte aligned. */
+#define ECCO_BF16 0
+#define ECCO_F16 1
+#define ECCO_F32 2
+#define ECCO_ROPE_INTERLEAVED 1
+#define ECCO_ROPE_INVERSE 2
+int ecco_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void* y, int64_t y_token_stride,
+              int64_t y_head_stride, int dtype, int64_t tokens, int heads, int dim, const float* table,
+              int64_t n_positions, int rotary_dim, const int32_t* positions, int flags, void* stream);
+
+/* Encodes the new tokens' keys and values into their pages: row cu_q[b] + i of
+ * k and v goes to position kv_lens[b] - (cu_q[b + 1] - cu_q[b]) + i of sequence
+ * b.  The blocks are those of ecco_select_encode.  With a rope_table the keys
+ * are first turned as by ecco_rope (bf16) and never written to memory; the
+ * angle's position is the token's own, or positions[row] if positions is not
+ * NULL.  Rows before cu_q[0] or behind cu_q[batch], positions below 0 or past
+ * the row's pages, and entries that name no page are skipped.
+ *   k, v        [tokens][kv_heads][128] bf16, strides in elements (multiples of
+ *               8), the 128 values contiguous, 16-byte aligned;
+ *   k_pages, v_pages  the pools, 16-byte aligned.  No page may appear twice
+ *               among the pages that the call writes to;
+ *   rotary_dim  as in ecco_rope with dim 128; ignored without a rope_table;
+ *   dev_stats   may be NULL. */
+int ecco_paged_append(const ecco_tables* k_tables, const ecco_tables* v_tables, ecco_paged paged,
+                      const uint16_t* k_bf16, int64_t k_token_stride, int64_t k_head_stride,
+                      const uint16_t* v_bf16, int64_t v_token_stride, int64_t v_head_stride, int64_t tokens,
+                      uint8_t* k_pages, uint8_t* v_pages, const float* rope_table, int64_t n_positions,
+                      int rotary_dim, const int32_t* positions, int flags, ecco_stats* dev_stats, void* stream);
+
+/* Attention of new tokens over the paged cache, in which they already are (a
+ * prompt's chunk, a single token, or both in one batch).  New token i of
+ * sequence b, with q = cu_q[b + 1] - cu_q[b] of them and n = kv_lens[b], sees
+ * the keys at positions s <= p = n - q + i, and with window > 0 only s > p -
+ * window.  For query head j (KV head j / group):
+ *   out[row][j][:] = sum_s p_s V~[s][:],  p = softmax_s(scale * (q[row][j] . K~[s])),
+ *   lse[row][j]    = log sum_s exp(scale * (q[row][j] . K~[s])),
+ * K~ and V~ the values ecco_decode would produce (a key whose page_table entry
+ * names no page counts as a block of zeros).  A row that sees no key (q > n)
+ * gets zeros and lse -inf; rows before cu_q[0] or behind cu_q[batch] are left
+ * as they were.  Scores, softmax statistics and sums are fp32; the weights p_s
+ * enter the second product as bf16, and the output is rounded to bf16.
+ *   q, out      [tokens][kv_heads * group][128] bf16, token and head strides in
+ *               elements (multiples of 8), 16-byte aligned;
+ *   lse         [tokens][kv_heads * group] fp32 contiguous, or NULL;
+ *   max_q, max_kv  bounds of the new tokens and of the keys of a sequence;
+ *               what lies past them (the last new tokens, the last keys) is
+ *               not computed and not seen;
+ *   group 1..16; batch * kv_heads * max_kv and tokens * kv_heads * group below 2^40;
+ *   workspace   caller-owned device scratch, 16-byte aligned, of
+ *               ecco_paged_attention_workspace_bytes(...) bytes; no initial
+ *               contents are needed.  Two calls that share it must be ordered.
+ * The blocks are decoded into the workspace (the KV heads in rounds of at most
+ * 1 GiB) and read from there by the tensor-core kernel. */
+size_t ecco_paged_attention_workspace_bytes(int batch, int kv_heads, int group, int max_q, int max_kv);
+int ecco_paged_attention(const ecco_tables* k_tables, const ecco_tables* v_tables, ecco_paged paged,
+                         const uint8_t* k_pages, const uint8_t* v_pages, const uint16_t* q_bf16,
+                         int64_t q_token_stride, int64_t q_head_stride, int group, int64_t tokens, int max_q,
+                         int max_kv, int window, float scale, uint16_t* out_bf16, int64_t out_token_stride,
+                         int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Copies page src[i] to page dst[i] of both pools, 0 <= i < n.  src and dst are
+ * HOST arrays, read before the call returns.  Every number in [0, n_pages), no
+ * destination twice, and no destination among the sources (ECCO_ERR_ARG).
+ * page_bytes = kv_heads * page_size * 64; pools 16-byte aligned. */
+int ecco_copy_pages(uint8_t* k_pages, uint8_t* v_pages, int64_t n_pages, int64_t page_bytes, const int32_t* src,
+                    const int32_t* dst, int64_t n, void* stream);
+
+/* Moves the kept tokens of every sequence together, in their order: the k-th
+ * token t < kv_lens[b] with keep[b][t] != 0 goes to position k of the pages
+ * dst_table[b], in both pools, and new_lens[b] becomes the number moved (no
+ * more than dst_max_pages * page_size; what is past that is left out).  The
+ * blocks are moved as they are.  The destination pages may not be among the
+ * pages read, nor appear twice; slots past new_lens[b] are left as they were.
+ * A token whose source or destination entry names no page is counted and not
+ * moved.  paged.cu_q is not used.
+ *   keep      [batch] rows of max_pages * page_size bytes or more, keep_stride
+ *             bytes apart; only the first kv_lens[b] of a row are read, and
+ *             none at or past keep_stride;
+ *   dst_table [batch][dst_max_pages] int32, dst_stride entries apart; keep,
+ *             dst_table and new_lens are device memory. */
+int ecco_compact_pages(ecco_paged paged, uint8_t* k_pages, uint8_t* v_pages, const uint8_t* keep,
+                       int64_t keep_stride, const int32_t* dst_table, int64_t dst_stride, int dst_max_pages,
+                       int32_t* new_lens, void* stream);
+
 /* Table learner on the GPU (offline; blocking; allocates and frees its own
  * temporaries; not for the hot path).  Learns one tensor's table blob -- the
  * per-tensor parameters the review page says are learned once, offline ("What

@@ -1,0 +1,546 @@
+"""The paged cache's operators on the GPU against plain 64-bit forms over the
+oracle's codec (tests/paged_reference.py, which derives the tolerances)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads as W
+import entropy_coded_kv_b200 as ecco
+from entropy_coded_kv_b200 import _lib
+from paged_reference import attend, bits, f64, pool_decode, rotate, rotate_f32
+from test_gpu_parity import inputs, table_set, to_dev_bf16
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+
+
+def i32(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ rotary positions
+def test_rope_table_values():
+    for rotary, scaling in ((128, None), (64, {"kind": "yarn", "factor": 16, "original": 8192}), (16, {"kind": "linear", "factor": 3})):
+        t = ecco.rope_table(131073, rotary, scaling=scaling).cpu().numpy()
+        f, m = ecco.rope_frequencies(rotary, scaling=scaling)
+        for p in (0, 1, 777, 65535, 131072):
+            a = p * np.asarray(f)
+            # one fp32 rounding of an fp64 value: half a step, and 2^-40 for fp64's own roundings of a far angle
+            for got, want in ((t[p, :, 0], m * np.cos(a)), (t[p, :, 1], m * np.sin(a))):
+                assert (np.abs(got - want) <= 2.0**-24 * np.abs(want) + 2.0**-36).all()
+
+
+ROPE = [
+    # tokens, heads, dim, rotary, interleaved, inverse, dtype
+    (1, 1, 128, 128, False, False, torch.bfloat16),
+    (7, 3, 128, 64, True, False, torch.bfloat16),
+    (33, 5, 256, 192, False, True, torch.float16),
+    (5, 2, 64, 16, True, True, torch.float32),
+    (3, 1, 1024, 1024, False, False, torch.float32),
+    (257, 8, 128, 96, False, False, torch.float16),
+    (2000, 32, 128, 128, True, False, torch.bfloat16),
+    (9, 4, 24, 16, False, False, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("tokens,heads,dim,rotary,inter,inv,dtype", ROPE)
+def test_rope(tokens, heads, dim, rotary, inter, inv, dtype):
+    g = torch.Generator().manual_seed(tokens)
+    x = torch.randn(tokens, heads, dim, generator=g).to(dtype)
+    pos = torch.randint(0, 5000, (tokens,), generator=g, dtype=torch.int32)
+    pos[0] = 4999
+    table = ecco.rope_table(5000, rotary)
+    y = ecco.rope(x.to(DEV), table, pos.to(DEV), interleaved=inter, inverse=inv).cpu()
+    tn = table.cpu().numpy()
+    want, size = rotate(x.double().numpy(), tn, pos.numpy(), rotary, inter, inv)
+    # two products and a sum, half a step of fp32 each, then half a step of the type
+    half = torch.finfo(dtype).eps / 2 if dtype != torch.float32 else 0.0
+    assert (np.abs(y.double().numpy() - want) <= 2.0**-24 * 2.01 * size + half * 1.01 * np.abs(want) + 1e-7 * (dtype == torch.float16)).all()
+    exact = torch.from_numpy(rotate_f32(x.float().numpy(), tn, pos.numpy(), rotary, inter, inv)).to(dtype)
+    assert torch.equal(y, exact)
+
+
+def test_rope_strides_in_place_and_far_positions():
+    g = torch.Generator(device=DEV).manual_seed(1)
+    table = ecco.rope_table(100, 64)
+    big = torch.randn(19, 6, 4, 160, generator=g, device=DEV).to(torch.bfloat16)
+    x = big[:, 1, :, 16:144]                     # a head's 128 values inside a wider row
+    pos = i32([-5, 1000] + list(range(17)))      # outside the table: its first and last row
+    clear = i32([0, 99] + list(range(17)))
+    want = ecco.rope(x.contiguous(), table, clear)
+    before = big.clone()
+    assert torch.equal(ecco.rope(x, table, pos), want)
+    out = torch.zeros(4, 19, 128, dtype=torch.bfloat16, device=DEV).transpose(0, 1)
+    assert ecco.rope(x, table, pos, out=out) is out and torch.equal(out, want)
+    assert torch.equal(big, before)
+    ecco.rope(x, table, pos, out=x)              # in place: only these values change
+    assert torch.equal(x, want)
+    before[:, 1, :, 16:144] = want
+    assert torch.equal(big, before)
+    assert ecco.rope(x[:0], table, pos[:0]).shape == (0, 4, 128)
+    # one token, one head: strides that say nothing
+    one = torch.randn(128, 3, device=DEV)[:, :1].t().unsqueeze(0).contiguous().to(torch.bfloat16)
+    assert ecco.rope(one, table, pos[:1]).shape == one.shape
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_gradient(inter):
+    """The turn is linear: its gradient is the turn back, by the formula and by differences."""
+    g = torch.Generator().manual_seed(3)
+    x, dy = torch.randn(11, 2, 64, generator=g), torch.randn(11, 2, 64, generator=g)
+    pos = torch.randint(0, 300, (11,), generator=g, dtype=torch.int32)
+    table = ecco.rope_table(300, 48)
+    tn = table.cpu().numpy()
+    got = ecco.rope(dy.to(DEV), table, pos.to(DEV), interleaved=inter, inverse=True).cpu().double().numpy()
+    i = np.arange(24)
+    ia, ib = (2 * i, 2 * i + 1) if inter else (i, i + 24)
+    cs, sn = (tn[pos.numpy(), :, k][:, None].astype(np.float64) for k in (0, 1))
+    d = dy.double().numpy()
+    want = d.copy()  # d/da of (a cos - b sin) da + (b cos + a sin) db, and d/db
+    want[..., ia], want[..., ib] = d[..., ia] * cs + d[..., ib] * sn, d[..., ib] * cs - d[..., ia] * sn
+    assert (np.abs(got - want) <= 2.0**-24 * 2.01 * (np.abs(want) + 2 * np.abs(d).max())).all()
+    f = lambda v: float((ecco.rope(v.to(DEV), table, pos.to(DEV), interleaved=inter).cpu().double() * dy.double()).sum())  # noqa: E731
+    for at in ((0, 0, 0), (3, 1, 30), (10, 0, 47), (5, 1, 60)):
+        h = torch.zeros_like(x)
+        h[at] = 8.0  # linear: a large step loses nothing but roundings (1408 values of size 10 at 2^-23)
+        assert abs((f(h) - f(-h)) / 16 - got[at]) <= 1408 * 10 * 2.0**-23
+
+
+# ------------------------------------------------------------------ append
+def meta(lens, new, page_size, n_pages, seed, width=None):
+    """(page_table, kv_lens, cu_q) with pages drawn at random, -1 past a sequence's pages."""
+    rng = np.random.default_rng(seed)
+    width = width or max(1, max(-(-n // page_size) for n in lens))
+    ids = list(rng.permutation(n_pages))
+    table = np.full((len(lens), width), -1, np.int32)
+    for b, n in enumerate(lens):
+        for i in range(-(-n // page_size)):
+            table[b, i] = ids.pop()
+    return table, np.asarray(lens, np.int32), np.cumsum([0] + list(new)).astype(np.int32)
+
+
+def encode_ref(blob, x):
+    return oracle.encode(blob, np.ascontiguousarray(x).reshape(-1, 128).reshape(-1), nthreads=8)
+
+
+APPEND = [
+    # new, lens, H, page, rotary, interleaved, k kind, v kind
+    ([1], [1], 1, 16, 128, False, "kv", "kv"),
+    ([1, 1, 1], [5, 64, 65], 8, 64, 128, False, "kv", "special"),
+    ([70, 0, 3, 200], [70, 9, 131, 450], 2, 48, 64, True, "special", "t5"),
+    ([33, 5], [40, 5], 3, 1, 32, False, "kv", "gauss"),
+    ([400], [1000], 4, 100, 0, False, "c1", "kv"),
+    ([17], [300], 5, 128, 96, True, "kv", "kv"),
+]
+
+
+@pytest.mark.parametrize("new,lens,H,page,rotary,inter,kk,vk", APPEND)
+def test_append_matches_the_oracle(new, lens, H, page, rotary, inter, kk, vk):
+    kt, vt = table_set("learned_kv"), table_set("random1")
+    T, n_pages = sum(new), sum(-(-n // page) for n in lens) + 2
+    table, kvl, cu = meta(lens, new, page, n_pages, seed=T)
+    pad = 3  # rows before the first sequence and behind the last: not read into any page
+    k = to_dev_bf16(inputs(kk, (T + 2 * pad) * H, seed=1).reshape(T + 2 * pad, H, 128))
+    v = to_dev_bf16(inputs(vk, (T + 2 * pad) * H, seed=2).reshape(T + 2 * pad, H, 128))
+    kp = torch.randint(0, 256, (n_pages, H, page, 64), dtype=torch.uint8, device=DEV)
+    vp = torch.randint(0, 256, (n_pages, H, page, 64), dtype=torch.uint8, device=DEV)
+    wk, wv = kp.cpu().numpy(), vp.cpu().numpy()
+    rt = ecco.rope_table(max(lens), rotary) if rotary else None
+    stats = ecco.new_stats(DEV)
+    ecco.paged_append(k, v, kp, vp, ecco.Tables(kt), ecco.Tables(vt), i32(table), i32(kvl), i32(cu + pad), rope=rt,
+                      interleaved=inter, stats=stats)
+    b = np.repeat(np.arange(len(new)), new)
+    pos = np.concatenate([np.arange(n - m, n) for n, m in zip(lens, new)]).astype(np.int64)
+    kb, vb = bits(k)[pad:pad + T], bits(v)[pad:pad + T]
+    if rotary:
+        turned = rotate_f32(f64(kb).astype(np.float32), rt.cpu().numpy(), pos, rotary, inter)
+        kb = bits(torch.from_numpy(turned).to(torch.bfloat16))
+    (ek, sk), (ev, sv) = encode_ref(kt, kb), encode_ref(vt, vb)
+    wk[table[b, pos // page], :, pos % page] = ek.reshape(T, H, 64)
+    wv[table[b, pos // page], :, pos % page] = ev.reshape(T, H, 64)
+    np.testing.assert_array_equal(kp.cpu().numpy(), wk)
+    np.testing.assert_array_equal(vp.cpu().numpy(), wv)
+    got = ecco.read_stats(stats)
+    for name in ("n_groups", "n_zero", "n_clipped", "n_padded", "n_records", "n_nonfinite", "payload_bits"):
+        assert got[name] == getattr(sk, name) + getattr(sv, name), name
+
+
+def test_append_strides_positions_and_bad_entries():
+    """k and v inside a fused projection's output, other angles than the
+    positions, and tokens that have no place: they leave the pools alone."""
+    kt = vt = table_set("learned_kv")
+    H, page, n_pages = 4, 16, 6
+    lens, new = [40, 3, 20], [8, 5, 4]          # the second: two of its tokens lie before position 0
+    table = np.array([[0, 1, 2], [3, -1, -1], [99, 4, -1]], np.int32)
+    cu = np.cumsum([0] + new).astype(np.int32)
+    qkv = to_dev_bf16(inputs("kv", 17 * 12, seed=5).reshape(17, 12, 128))
+    k, v = qkv[:, 4:8], qkv[:, 8:12]
+    pos = np.arange(100, 117).astype(np.int32)
+    rt = ecco.rope_table(110, 128)
+    kp = torch.randint(0, 256, (n_pages, H, page, 64), dtype=torch.uint8, device=DEV)
+    vp = kp.clone()
+    wk, wv = kp.cpu().numpy(), vp.cpu().numpy()
+    ecco.paged_append(k, v, kp, vp, ecco.Tables(kt), ecco.Tables(vt), i32(table), i32(lens), i32(cu), rope=rt, positions=i32(pos))
+    turned = rotate_f32(f64(bits(k)).astype(np.float32), rt.cpu().numpy(), pos, 128, False)
+    ek = encode_ref(kt, bits(torch.from_numpy(turned).to(torch.bfloat16)))[0].reshape(17, H, 64)
+    ev = encode_ref(vt, bits(v))[0].reshape(17, H, 64)
+    for b in range(3):
+        for i in range(new[b]):
+            p = lens[b] - new[b] + i
+            if p < 0 or not 0 <= table[b, p // page] < n_pages:
+                continue
+            wk[table[b, p // page], :, p % page] = ek[cu[b] + i]
+            wv[table[b, p // page], :, p % page] = ev[cu[b] + i]
+    np.testing.assert_array_equal(kp.cpu().numpy(), wk)
+    np.testing.assert_array_equal(vp.cpu().numpy(), wv)
+    # lengths past the row's pages, and below zero
+    for bad in (1000, -3, 2**31 - 1, -2**31):
+        ecco.paged_append(k[:1], v[:1], kp, vp, ecco.Tables(kt), ecco.Tables(vt), i32(table[:1]), i32([bad]), i32([0, 1]))
+    np.testing.assert_array_equal(kp.cpu().numpy(), wk)
+
+
+# ------------------------------------------------------------------ attention
+def fill_pool(blob, n_pages, H, page, kind, seed):
+    b, _ = oracle.encode(blob, inputs(kind, n_pages * H * page, seed=seed), nthreads=8)
+    return b.reshape(n_pages, H, page, 64)
+
+
+ATTEND = [
+    # new, lens, H, G, page, window, scale, K tables, V tables, K kind, V kind
+    ([1], [1], 1, 1, 16, 0, 0.0884, "learned_kv", "learned_kv", "kv", "kv"),
+    ([1], [650], 2, 4, 16, 0, 0.0884, "learned_kv", "learned_kv", "kv", "kv"),
+    ([1, 1, 1, 1], [127, 128, 129, 1000], 2, 4, 64, 0, 0.0884, "learned_kv", "random1", "kv", "kv"),
+    ([64], [64], 1, 4, 64, 0, 0.0884, "learned_kv", "learned_kv", "kv", "kv"),
+    ([65, 1, 0, 33], [65, 300, 17, 200], 2, 5, 48, 0, 0.0884, "random0", "learned_kv", "gauss", "kv"),
+    ([129], [700], 1, 8, 100, 0, 0.0884, "learned_kv", "learned_kv", "kv", "t5"),
+    ([40, 7], [350, 129], 1, 3, 1, 100, 0.0884, "learned_kv", "learned_kv", "kv", "kv"),
+    ([200, 1], [600, 513], 2, 2, 128, 130, -0.05, "learned_kv", "learned_kv", "kv", "kv"),
+    ([5, 3], [2, 0], 2, 4, 16, 0, 0.0884, "learned_kv", "learned_kv", "kv", "kv"),     # rows that see nothing
+    ([3], [260], 1, 16, 33, 1, 0.0884, "learned_kv", "learned_kv", "kv", "kv"),        # a window of one: the values themselves
+    ([10], [150], 3, 7, 16, 0, 0.0, "learned_kv", "learned_kv", "kv", "kv"),           # scale 0: the mean
+    ([30], [257], 1, 4, 24, 0, 0.0884, "random3", "random2", "special", "special"),
+    ([300], [300], 1, 1, 64, 0, 1.0, "learned_kv", "learned_kv", "kv", "kv"),          # scores of hundreds
+]
+
+
+def run_attention(kb, vb, kt, vt, q, table, lens, cu, scale, **kw):
+    lse = torch.full(q.shape[:2], 7.0, dtype=torch.float32, device=DEV)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    got = ecco.paged_attention(q, torch.from_numpy(kb).to(DEV), torch.from_numpy(vb).to(DEV), ecco.Tables(kt), ecco.Tables(vt),
+                               i32(table), i32(lens), i32(cu), scale, out=out, lse=lse, **kw)
+    assert got is out
+    return f64(bits(out)), lse.cpu().double().numpy()
+
+
+def check_attention(out, lse, ref):
+    want, wlse, tol, tol_lse, written = ref
+    assert (out[~written] == 7.0).all() and (lse[~written] == 7.0).all()
+    out, lse, want, wlse, tol, tol_lse = (a[written] for a in (out, lse, want, wlse, tol, tol_lse))
+    assert np.isfinite(out).all()
+    err = np.abs(out - want)
+    assert (err <= tol).all(), f"worst excess {(err / np.maximum(tol, 1e-38)).max():.3f} of the tolerance"
+    none = np.isneginf(wlse)
+    assert np.isneginf(lse[none]).all() and (out[none] == 0).all()
+    assert (np.abs(lse - wlse)[~none] <= tol_lse[~none]).all()
+
+
+@pytest.mark.parametrize("new,lens,H,G,page,window,scale,ktn,vtn,kk,vk", ATTEND)
+def test_attention(new, lens, H, G, page, window, scale, ktn, vtn, kk, vk):
+    kt, vt = table_set(ktn), table_set(vtn)
+    n_pages = sum(-(-n // page) for n in lens) + 1
+    table, kvl, cu = meta(lens, new, page, n_pages, seed=len(lens) + page)
+    kb, vb = fill_pool(kt, n_pages, H, page, kk, 3), fill_pool(vt, n_pages, H, page, vk, 4)
+    pad = 2
+    T = sum(new) + 2 * pad
+    q = torch.randn(T, H * G, 128, generator=torch.Generator().manual_seed(T)).to(torch.bfloat16).to(DEV)
+    out, lse = run_attention(kb, vb, kt, vt, q, table, kvl, cu + pad, scale, window=window)
+    ref = attend(f64(bits(q)), pool_decode(kt, kb), pool_decode(vt, vb), table, kvl, cu + pad, scale, window)
+    check_attention(out, lse, ref)
+
+
+def test_attention_bounds_garbage_and_bad_pages():
+    """Random bytes as blocks, entries that name no page, lengths past the row's
+    pages, and bounds below what the arrays say."""
+    kt, vt = table_set("learned_kv"), table_set("random1")
+    rng = np.random.default_rng(8)
+    H, G, page, n_pages = 2, 4, 24, 20
+    kb, vb = (rng.integers(0, 256, (n_pages, H, page, 64), dtype=np.uint8) for _ in range(2))
+    table = rng.permutation(n_pages)[:18].reshape(3, 6).astype(np.int32)
+    table[0, 2], table[1, 5], table[2, 0] = -1, n_pages, 2**31 - 1
+    lens, new = np.array([140, 1000, 130], np.int32), [20, 9, 1]
+    cu = np.cumsum([0] + new).astype(np.int32)
+    q = torch.randn(30, H * G, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
+    kd, vd = pool_decode(kt, kb), pool_decode(vt, vb)
+    for max_q, max_kv in ((20, 144), (20, 131), (7, 144), (1, 1), (20, 0)):
+        out, lse = run_attention(kb, vb, kt, vt, q, table, lens, cu, 1e-3, max_q=max_q, max_kv=max_kv)
+        check_attention(out, lse, attend(f64(bits(q)), kd, vd, table, lens, cu, 1e-3, 0, max_q, max_kv))
+    # arrays that make no sense stay inside the buffers and write no row twice
+    for bad_lens, bad_cu in (([-5, 2**31 - 1, -2**31], cu), (lens, [0, 40, 60, 90]), (lens, [-7, 3, 2, 30])):
+        run_attention(kb, vb, kt, vt, q, table, bad_lens, bad_cu, 1e-3)
+        torch.cuda.synchronize()
+
+
+def test_attention_nan_query_and_strides():
+    """A NaN or infinite query spoils its own row only; q and out inside wider arrays."""
+    kt = vt = table_set("learned_kv")
+    H, G, page, lens, new = 2, 4, 16, [200], [40]
+    table, kvl, cu = meta(lens, new, page, 14, seed=1)
+    kb, vb = fill_pool(kt, 14, H, page, "kv", 3), fill_pool(vt, 14, H, page, "kv", 4)
+    wide = torch.randn(40, 3, H * G, 136, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).to(DEV)
+    q = wide[:, 1, :, 8:]
+    clean = ecco.paged_attention(q.contiguous(), torch.from_numpy(kb).to(DEV), torch.from_numpy(vb).to(DEV), ecco.Tables(kt),
+                                 ecco.Tables(vt), i32(table), i32(kvl), i32(cu), 0.0884)
+    q[7, 3, 5], q[11, 0, 0] = float("nan"), float("inf")
+    home = torch.zeros(H * G, 40, 144, dtype=torch.bfloat16, device=DEV)
+    out = home.transpose(0, 1)[..., :128]
+    ecco.paged_attention(q, torch.from_numpy(kb).to(DEV), torch.from_numpy(vb).to(DEV), ecco.Tables(kt), ecco.Tables(vt),
+                         i32(table), i32(kvl), i32(cu), 0.0884, out=out)
+    assert out[7, 3].isnan().all()
+    same = torch.ones(40, H * G, dtype=torch.bool, device=DEV)
+    same[7, 3] = same[11, 0] = False
+    assert torch.equal(out[same], clean[same]) and (home[..., 128:] == 0).all()
+
+
+def test_attention_masked_slots_never_count():
+    """Blocks past a sequence's length, in its last page and in pages behind it, change nothing."""
+    kt = vt = table_set("learned_kv")
+    H, G, page, lens, new = 1, 4, 64, [130, 70], [3, 70]
+    table, kvl, cu = meta(lens, new, page, 9, seed=2, width=4)
+    table[table < 0] = 9  # a tenth page, no sequence's own
+    kb, vb = fill_pool(kt, 10, H, page, "kv", 3), fill_pool(vt, 10, H, page, "kv", 4)
+    q = torch.randn(73, G, 128, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(DEV)
+    a = run_attention(kb, vb, kt, vt, q, table, kvl, cu, 0.0884)
+    rng = np.random.default_rng(0)
+    for b in range(2):
+        for i in range(lens[b], table.shape[1] * page):
+            kb[table[b, i // page], :, i % page] = rng.integers(0, 256, (H, 64))
+            vb[table[b, i // page], :, i % page] = rng.integers(0, 256, (H, 64))
+    b = run_attention(kb, vb, kt, vt, q, table, kvl, cu, 0.0884)
+    np.testing.assert_array_equal(a[0], b[0])
+    np.testing.assert_array_equal(a[1], b[1])
+
+
+def test_single_token_matches_decode_attention():
+    """One token a sequence over equal lengths is the framework's decode-phase
+    attention: both within their tolerances of one 64-bit reference, so of each
+    other within the sum."""
+    kt = vt = table_set("learned_kv")
+    B, H, G, S, page = 3, 2, 4, 1000, 40
+    kb, vb = fill_pool(kt, B, H, S, "kv", 3), fill_pool(vt, B, H, S, "kv", 4)
+    kp, vp = (x.reshape(B, H, S // page, page, 64).transpose(0, 2, 1, 3, 4).reshape(-1, H, page, 64).copy() for x in (kb, vb))
+    table = np.arange(B * (S // page), dtype=np.int32).reshape(B, -1)
+    q = torch.randn(B, H * G, 128, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(DEV)
+    out, _ = run_attention(kp, vp, kt, vt, q, table, [S] * B, np.arange(B + 1), 0.0884)
+    t = ecco.Tables(kt)
+    other = ecco.decode_attention(torch.from_numpy(kb).to(DEV), torch.from_numpy(vb).to(DEV), t, t, q, S, 0.0884).cpu().double().numpy()
+    ref = attend(f64(bits(q)), pool_decode(kt, kp), pool_decode(vt, vp), table, [S] * B, np.arange(B + 1), 0.0884, 0)
+    assert (np.abs(out - other) <= ref[2] + 1e-3 * ref[2] * 2.0**8).all()
+
+
+# ------------------------------------------------------------------ pages
+@pytest.mark.parametrize("pairs,H,page", [(1, 1, 1), (5, 8, 16), (4000, 1, 3), (7, 3, 100)])
+def test_copy_pages(pairs, H, page):
+    rng = np.random.default_rng(pairs)
+    n = 2 * pairs + 1
+    kp, vp = (torch.from_numpy(rng.integers(0, 256, (n, H, page, 64), dtype=np.uint8)).to(DEV) for _ in range(2))
+    order = rng.permutation(n).astype(np.int32)
+    src, dst = order[:pairs].copy(), order[pairs:2 * pairs]
+    src[pairs // 2:] = src[0]  # one source for many
+    wk, wv = kp.clone(), vp.clone()
+    for w, p in ((wk, kp), (wv, vp)):
+        w[torch.from_numpy(dst).long()] = p[torch.from_numpy(src).long()]
+    ecco.copy_pages(kp, vp, torch.from_numpy(src), dst.tolist())
+    assert torch.equal(kp, wk) and torch.equal(vp, wv)
+
+
+@pytest.mark.parametrize("lens,H,page,kept", [([1], 1, 16, 1.0), ([0, 5], 2, 16, 0.5), ([3000, 1, 1024, 1025], 3, 48, 0.5),
+                                              ([2500], 2, 7, 0.02), ([700, 650], 8, 64, 0.0), ([1024], 1, 128, 1.0)])
+def test_compact_pages(lens, H, page, kept):
+    rng = np.random.default_rng(sum(lens))
+    width = max(1, max(-(-n // page) for n in lens))
+    n_pages = 2 * len(lens) * width + 1
+    kp, vp = (torch.from_numpy(rng.integers(0, 256, (n_pages, H, page, 64), dtype=np.uint8)).to(DEV) for _ in range(2))
+    ids = rng.permutation(n_pages)[:2 * len(lens) * width].reshape(2, len(lens), width).astype(np.int32)
+    keep = rng.random((len(lens), width * page)) < kept
+    wk, wv = kp.cpu().numpy(), vp.cpu().numpy()
+    want = []
+    for b, n in enumerate(lens):
+        t = np.flatnonzero(keep[b, :n])
+        k = np.arange(len(t))
+        for w in (wk, wv):
+            w[ids[1, b, k // page], :, k % page] = w[ids[0, b, t // page], :, t % page]
+        want.append(len(t))
+    got = ecco.compact_pages(kp, vp, i32(ids[0]), i32(lens), torch.from_numpy(keep).to(DEV), i32(ids[1]))
+    assert got.tolist() == want
+    np.testing.assert_array_equal(kp.cpu().numpy(), wk)
+    np.testing.assert_array_equal(vp.cpu().numpy(), wv)
+
+
+def test_compact_bounds():
+    """Too few destination pages, entries that name no page, lengths past the row, a short mask."""
+    rng = np.random.default_rng(4)
+    kp, vp = (torch.from_numpy(rng.integers(0, 256, (10, 2, 8, 64), dtype=np.uint8)).to(DEV) for _ in range(2))
+    table, dst = np.array([[0, -1, 2, 10]], np.int32), np.array([[5, 77, 6]], np.int32)
+    keep = np.ones((1, 30), np.uint8)
+    wk = kp.cpu().numpy()
+    for t in range(24):  # 30 tokens counted (the mask's end), room for 24; page 1 of the source and of the destination are missing
+        if t // 8 != 1:
+            wk[dst[0, t // 8], :, t % 8] = wk[table[0, t // 8], :, t % 8]
+    got = ecco.compact_pages(kp, vp, i32(table), i32([1000]), torch.from_numpy(keep).to(DEV), i32(dst))
+    assert got.tolist() == [24]
+    np.testing.assert_array_equal(kp.cpu().numpy(), wk)
+
+
+# ------------------------------------------------------------------ together
+def test_cache_from_prompt_to_fork_to_compaction():
+    """A run as a server makes it: prompts in chunks, single tokens, a fork whose
+    copies diverge, dropped tokens, a freed sequence.  Every attention is
+    checked against the 64-bit form over a plain list of (turned, encoded)
+    tokens of each sequence."""
+    H, G, page, layers, rotary = 2, 4, 16, 2, 64
+    blobs = [(table_set("learned_kv"), table_set("random1")), (table_set("random0"), table_set("learned_kv"))]
+    cache = ecco.PagedCache(40, page, H, [ecco.Tables(a) for a, _ in blobs], [ecco.Tables(b) for _, b in blobs])
+    cache.k_pages.random_(0, 256)
+    cache.v_pages.random_(0, 256)
+    table = ecco.rope_table(1000, rotary, scaling={"kind": "yarn", "factor": 4, "original": 200})
+    tn = table.cpu().numpy()
+    g = torch.Generator().manual_seed(9)
+    tokens = {}  # sequence -> per layer (k, v) fp64 [n, H, 128]
+    position = {}
+
+    def step(seqs, new):
+        st = cache.extend(seqs, new)
+        T = sum(new)
+        pos = np.concatenate([np.arange(position[s], position[s] + n) for s, n in zip(seqs, new)])
+        assert st.positions.tolist() == pos.tolist() and st.tokens == T
+        for s, n in zip(seqs, new):
+            position[s] += n
+        for layer in range(layers):
+            qkv = (torch.randn(T, (G + 2) * H, 128, generator=g) * 2).to(torch.bfloat16).to(DEV)
+            q, k, v = qkv.split([G * H, H, H], 1)
+            cache.append(st, layer, k, v, rope=table)
+            qr = ecco.rope(q, table, st.positions)
+            lse = torch.empty(T, G * H, device=DEV)
+            out = cache.attend(st, layer, qr, 0.0884, lse=lse)
+            turned = rotate_f32(f64(bits(k)).astype(np.float32), tn, pos, rotary, False)
+            kb, vb = bits(torch.from_numpy(turned).to(torch.bfloat16)), bits(v)
+            new_k, new_v = (f64(np.asarray(oracle.decode(t, encode_ref(t, x)[0]))).reshape(T, H, 128)
+                            for t, x in zip(blobs[layer], (kb, vb)))
+            at = 0
+            for s, n in zip(seqs, new):
+                old = tokens[s][layer]
+                tokens[s][layer] = tuple(np.concatenate([a, b[at:at + n]]) for a, b in zip(old, (new_k, new_v)))
+                kk, vv = tokens[s][layer]
+                ref = attend(f64(bits(qr))[at:at + n], kk[None].transpose(0, 2, 1, 3), vv[None].transpose(0, 2, 1, 3),
+                             np.zeros((1, 1), int), [len(kk)], [0, n], 0.0884, 0) if len(kk) else None
+                if ref is not None and n:
+                    check_attention(f64(bits(out))[at:at + n], lse.cpu().double().numpy()[at:at + n], ref)
+                at += n
+
+    def fresh():
+        s = cache.add()
+        tokens[s], position[s] = [(np.zeros((0, H, 128)),) * 2 for _ in range(layers)], 0
+        return s
+
+    a, b = fresh(), fresh()
+    step([a, b], [37, 5])
+    step([b, a], [20, 1])
+    step([a, b], [0, 1])
+    c = cache.fork(a)
+    tokens[c], position[c] = [tuple(t) for t in tokens[a]], position[a]
+    assert cache.book.pages(c) == cache.book.pages(a)
+    step([a, c, b], [3, 2, 1])                       # the shared last page parts
+    assert cache.book.pages(c)[:-1] == cache.book.pages(a)[:-1] and cache.book.pages(c)[-1] != cache.book.pages(a)[-1]
+    step([c], [40])
+    keep = torch.rand(2, 128, generator=g) < 0.4
+    lens = cache.compact([c, b], keep.to(DEV))
+    for s, row, n in zip((c, b), keep.numpy(), lens):
+        tokens[s] = [tuple(x[row[:len(x)]] for x in layer) for layer in tokens[s]]
+        assert cache.length(s) == n == len(tokens[s][0][0])
+    step([a, b, c], [1, 1, 30])
+    free = cache.book.free_pages
+    cache.free(a)
+    assert cache.book.free_pages > free
+    d = fresh()
+    step([d, c, b], [50, 1, 1])
+    with pytest.raises(ecco.OutOfPages):
+        cache.extend([d], [10000])
+    step([d], [1])
+
+
+def test_captured_step_replays_on_new_lengths_and_streams():
+    """Append and attention captured into a graph on a side stream; replays
+    follow the page table and lengths written between them.  Two graphs share
+    one workspace, replayed in order."""
+    kt = vt = table_set("learned_kv")
+    H, G, page, n_pages, B = 2, 4, 16, 40, 2
+    kT, vT = ecco.Tables(kt), ecco.Tables(vt)
+    kp, vp = (torch.from_numpy(fill_pool(kt, n_pages, H, page, "kv", s)).to(DEV) for s in (3, 4))
+    table = np.random.default_rng(1).permutation(n_pages)[:30].reshape(2, 15).astype(np.int32)
+    tb, lens, cu = i32(table), i32([10, 20]), i32([0, 1, 2])
+    k, v, q = (torch.randn(B, n, 128, device=DEV).to(torch.bfloat16) for n in (H, H, H * G))
+    ws = torch.empty(ecco.paged_attention_workspace_bytes(B, H, G, 1, 240), dtype=torch.uint8, device=DEV)
+    rt = ecco.rope_table(240, 128)
+    outs = [torch.empty_like(q) for _ in range(2)]
+    side, graphs = torch.cuda.Stream(), []
+
+    def once(o):
+        ecco.paged_append(k, v, kp, vp, kT, vT, tb, lens, cu, rope=rt)
+        ecco.paged_attention(q, kp, vp, kT, vT, tb, lens, cu, 0.0884, max_q=1, max_kv=240, out=o, workspace=ws)
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        once(outs[0])
+        for o in outs:
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr, stream=side):
+                once(o)
+            graphs.append(gr)
+        for n in ([10, 20], [11, 21], [240, 1], [128, 129]):
+            lens.copy_(i32(n))
+            k.copy_(torch.randn_like(k, dtype=torch.float32))
+            for gr in graphs:
+                gr.replay()
+            side.synchronize()
+            assert torch.equal(outs[0], outs[1])
+            ref = attend(f64(bits(q)), pool_decode(kt, kp.cpu().numpy()), pool_decode(vt, vp.cpu().numpy()), table, n, [0, 1, 2], 0.0884, 0)
+            assert (np.abs(f64(bits(outs[0])) - ref[0]) <= ref[2]).all()
+    torch.cuda.current_stream().wait_stream(side)
+
+
+def test_refusals_of_the_binding():
+    t = ecco.Tables(table_set("learned_kv"))
+    kp = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, device=DEV)
+    tb, lens, cu = i32([[0, 1]]), i32([5]), i32([0, 5])
+    x = torch.zeros(5, 2, 128, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(5, 8, 128, dtype=torch.bfloat16, device=DEV)
+    ok = dict(k_pages=kp, v_pages=kp.clone(), k_tables=t, v_tables=t, page_table=tb, kv_lens=lens, cu_q=cu)
+    bad = [dict(k_pages=kp.float()), dict(v_pages=kp[:, :, :8]), dict(k_pages=kp[:2]), dict(page_table=tb.long()), dict(page_table=tb[0]),
+           dict(kv_lens=i32([1, 2])), dict(cu_q=i32([0])), dict(kv_lens=lens.cpu()), dict(page_table=i32([[0], [1]]).t())]
+    for b in bad:
+        with pytest.raises((TypeError, ValueError)):
+            if "page_table" in b and b["page_table"].dim() == 2 and b["page_table"].dtype == torch.int32:
+                b = {**b, "page_table": i32([[0, 9], [1, 9]]).t()[:1]}
+            ecco.paged_append(x, x, **{**ok, **b})
+    for b in (dict(k=x.float()), dict(v=x[:3]), dict(k=x[..., :64]), dict(rope=torch.zeros(4, 8, device=DEV)),
+              dict(positions=i32([1])), dict(stats=torch.zeros(2, dtype=torch.int64, device=DEV))):
+        with pytest.raises((TypeError, ValueError)):
+            ecco.paged_append(**{**dict(k=x, v=x), **ok, **b})
+    with pytest.raises(ecco.EccoError):   # a table of more than 128 values
+        ecco.paged_append(x, x, **ok, rope=ecco.rope_table(4, 256))
+    for b in (dict(q=q[:, :7]), dict(q=q.half()), dict(out=q.float()), dict(lse=torch.zeros(5, 7, device=DEV))):
+        with pytest.raises((TypeError, ValueError)):
+            ecco.paged_attention(**{**dict(q=q, scale=1.0), **ok, **b})
+    for b in (dict(scale=float("nan")), dict(window=-1), dict(max_q=-1), dict(max_kv=-1), dict(workspace=torch.zeros(64, dtype=torch.uint8, device=DEV)),
+              dict(out=q[:, :1].expand(5, 8, 128)), dict(q=torch.zeros(5, 2 * 17, 128, dtype=torch.bfloat16, device=DEV))):
+        with pytest.raises(ecco.EccoError):
+            ecco.paged_attention(**{**dict(q=q, scale=1.0), **ok, **b})
+    with pytest.raises(ecco.EccoError):
+        ecco.copy_pages(kp, kp.clone(), [0, 1], [2, 2])
+    with pytest.raises(TypeError):
+        ecco.copy_pages(kp, kp.clone(), i32([0]), [1])
+    with pytest.raises(ValueError):
+        ecco.compact_pages(kp, kp.clone(), tb, lens, torch.ones(2, 9, dtype=torch.bool, device=DEV), tb)
