@@ -514,7 +514,11 @@ cudaError_t launch_wait_timeout_selftest(cudaStream_t s)
 extern "C" int ecco_device_timeouts(unsigned int* out)
 {
     if (!out) return ECCO_ERR_ARG;
-    if (cudaMemcpyFromSymbol(out, ecco::g_timeouts, sizeof(unsigned int)) != cudaSuccess) return ECCO_ERR_CUDA;
+    unsigned int paged = 0;
+    if (cudaMemcpyFromSymbol(out, ecco::g_timeouts, sizeof(unsigned int)) != cudaSuccess ||
+        ecco::paged_timeouts(&paged) != cudaSuccess)
+        return ECCO_ERR_CUDA;
+    *out += paged;
     if (int* f = ecco::timeout_flag()) *reinterpret_cast<volatile int*>(f) = 0;
     return ECCO_OK;
 }

@@ -87,6 +87,7 @@ cudaError_t launch_decode_multi(const ecco_segment* segs, int n, cudaStream_t s)
 // (mapped pinned memory, allocated once) that a wait which gave up raises.
 int* timeout_flag();
 bool timeout_raised();
+cudaError_t paged_timeouts(unsigned int* n);  // the paged attention's count, current device
 cudaError_t launch_wait_timeout_selftest(cudaStream_t s);
 // Activation format: 64-value groups (the descriptor counts 64-value groups).
 cudaError_t launch_encode_act(const ecco_tables* t, const uint16_t* x, const ecco_desc& d,

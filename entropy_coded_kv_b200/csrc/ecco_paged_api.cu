@@ -158,6 +158,7 @@ extern "C" int ecco_paged_attention(const ecco_tables* kt, const ecco_tables* vt
     if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(ws, 16))
         return ECCO_ERR_ALIGN;
+    if (timeout_raised()) return ECCO_ERR_TIMEOUT;  // an earlier tensor-core launch gave up
     const PagedAttnArgs a{p, {kt->d, vt->d}, {k_pages, v_pages}, q, out, lse, q_token, q_head, out_token, out_head,
                           tokens, group, max_q, max_kv, std::min(window, 1 << 30), scale};
     return status(launch_paged_attention(a, ws, (cudaStream_t)stream));

@@ -224,6 +224,25 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
 }
 
 // ------------------------------------------------------------ attention
+// Persistent kernel, one CTA an SM.  An item is (sequence, KV head, 256 rows),
+// a row being (new token, query head of the group), so that a tile of keys
+// serves every query head that shares it.  Items cost as many units as the
+// 128-key tiles their rows see (at least one); the units of all items, in one
+// line, are cut into equal shares, so a CTA's share may begin and end inside
+// items: such parts leave (O, max, sum) in the workspace, and a second kernel
+// joins them.  The cut needs no rule for the number of splits, and prompts
+// with triangular costs, ragged batches and single tokens over a long cache
+// all fill the SMs alike.
+//
+// Inside an item, two row tiles of 128 alternate on the tensor cores:
+//   S_i = Q_i K_j^T   (128 x 128 x 128, both from shared memory, into TMEM)
+//   P_i = exp2(c S_i - c m), one thread a row, back to TMEM as bf16 over S_i
+//   O_i += P_i V_j    (P from TMEM, V as it lies: rows of keys, N-major)
+// Warps 0-3 and 4-7 hold the rows of tile 0 and 1, lane = TMEM lane; warp 8
+// issues the products, warp 9 the copies (a tile is one 32 KB bulk copy).
+// The maximum m is only moved, and O rescaled, when a row's new maximum is
+// above it by more than 2^8: until then the weights stay below 2^8 and sum and
+// products are as exact as with the true maximum.
 struct AttnArgs {
     ecco_paged p;
     Bounds w;
@@ -234,66 +253,651 @@ struct AttnArgs {
     int64_t q_token, q_head, out_token, out_head;
     int group, h0, hn;
     float scale;
+    // partial results: slots 2c (a share's part of an item begun before it) and
+    // 2c + 1 (an item that goes on in the next share) of CTA c
+    float* part_o;   // [slot][32][slot_rows] float4
+    float* part_ml;  // [slot][2][slot_rows]: maximum (in units of log2), sum
+    int4* part_item; // [CTA]: sequence, head, row tile, last CTA of the item begun in this share and unfinished; head < 0: none
+    int slot_rows;
+    int* flag;
 };
 
-constexpr int kWarps = 8;
+constexpr int kRows = 256;               // rows of an item
+constexpr int kAttnThreads = 384;
+constexpr int kStages = 4;               // K and V tiles in flight
+constexpr int kMaxCtas = 160;            // shares (and twice as many slots) at most
+constexpr int kBars = 2 * kStages + 9;
+constexpr size_t kOffRing = 2 * kTileBytes;
+constexpr size_t kOffBars = kOffRing + (size_t)kStages * kTileBytes;
+constexpr size_t kOffUnits = kOffBars + kBars * 8 + 56;
+constexpr size_t kOffSeq = kOffUnits + (ECCO_MAX_BATCH + 1) * 8 + 8;
+constexpr size_t kAttnSmem = 1024 + kOffSeq + sizeof(int) * (5 * ECCO_MAX_BATCH + 1);
+constexpr uint32_t kSpinLimit = 1u << 20;
 
-// One warp a (row, query head): lane l holds values 4 l .. 4 l + 3.
-__global__ void __launch_bounds__(kWarps * 32) paged_attention_kernel(const __grid_constant__ AttnArgs A)
+__device__ unsigned int g_timeouts = 0;
+
+// D fp32, A and B bf16, N = 128, M = 128; kIdescPV: B N-major (bit 16).
+constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+
+// Shared-memory matrix descriptor with the 128-byte swizzle (layout type 2):
+// 8-row groups 1024 bytes apart; leading offset = the distance between the
+// 64-value halves (used where the values run along N).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t addr)
 {
-    __shared__ int s_cu[ECCO_MAX_BATCH + 1], s_first[ECCO_MAX_BATCH];
-    const int tid = threadIdx.x, lane = tid & 31;
-    for (int b = tid; b < A.p.batch; b += kWarps * 32) {
+    return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)((kTileBytes / 2) >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Waits for the phase of the given parity: at most kSpinLimit polls of up to a
+// microsecond.  A wait that gives up counts itself, raises the host-visible
+// flag and marks the CTA dead, so that its other waits end too.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead, int* flag)
+{
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(1000u)
+            : "memory");
+        if (done) return true;
+        if (*dead) return false;
+    }
+    *dead = 1u;
+    atomicAdd(&g_timeouts, 1u);
+    if (flag) {
+        *reinterpret_cast<volatile int*>(flag) = 1;
+        __threadfence_system();
+    }
+    return false;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kIdescQK), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(kIdescPV), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+#define ECCO_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
+#define ECCO_I8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+
+// 32 columns of this warp's 32 lanes; the registers hold them after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : ECCO_R8(v, 0), ECCO_R8(v, 8), ECCO_R8(v, 16), ECCO_R8(v, 24)
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::ECCO_I8(v, 0),
+        ECCO_I8(v, 8), ECCO_I8(v, 16), ECCO_I8(v, 24), "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The tiles [t0, t0 + n) that rows 256 qt .. of the sequence see, and its rows.
+struct Span {
+    int t0, n, rows;
+};
+
+__device__ __forceinline__ Span span_of(const Seq& s, int group, int window, int qt)
+{
+    Span r;
+    const int r0 = qt * kRows;
+    r.rows = min(kRows, s.q * group - r0);
+    int lo, hi;
+    visible(s, window, r0 / group, (r0 + r.rows - 1) / group, lo, hi);
+    r.t0 = lo / kTile;
+    r.n = hi > lo ? (hi + kTile - 1) / kTile - r.t0 : 0;
+    return r;
+}
+
+struct Plan {  // in shared memory
+    long long* units;  // [batch + 1] units before sequence b, over the round's heads
+    int *q0, *q, *base, *keys, *tile;  // tile: scratch tile of (head 0, key tile 0) of sequence b
+    int batch, tiles;
+    __device__ __forceinline__ Seq seq(int b) const { return Seq{q0[b], q[b], base[b], keys[b]}; }
+};
+
+// One part of an item: key tiles [t0, t0 + n) of its rows.
+struct Part {
+    int b, h, qt, rows, t0, n;
+    bool begins, ends;  // the item's first / last tiles are among them
+    long long at;       // the item's first unit
+    int units;          // of the item
+};
+
+// Walks a share's parts.  Every warp runs its own copy.
+struct Walk {
+    const Plan& P;
+    int group, window, hn;
+    long long at, stop;  // next unit, end of the share
+    int b, h, qt, skip;  // item of unit `at`, units of it before `at`
+
+    __device__ __forceinline__ bool next(Part& x)
+    {
+        if (at >= stop) return false;
+        Seq s = P.seq(b);
+        while (qt * kRows >= s.q * group) {  // the sequence's rows are done: its next head, or the next sequence with rows
+            qt = 0;
+            if (s.q > 0 && ++h < hn) break;
+            h = 0;
+            s = P.seq(++b);
+        }
+        const Span r = span_of(s, group, window, qt);
+        const int units = max(1, r.n);
+        const int take = (int)min((long long)(units - skip), stop - at);
+        x.b = b;
+        x.h = h;
+        x.qt = qt;
+        x.rows = r.rows;
+        x.t0 = r.t0 + skip;
+        x.n = min(take, r.n - skip);
+        x.begins = skip == 0;
+        x.ends = skip + take == units;
+        x.at = at - skip;
+        x.units = units;
+        at += take;
+        skip = 0;
+        ++qt;
+        return true;
+    }
+};
+
+__global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const __grid_constant__ AttnArgs A)
+{
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
+    const uint32_t bars = smem_u32(smem + kOffBars);
+    const uint32_t bar_full = bars, bar_empty = bars + 8 * kStages, bar_q = bars + 16 * kStages, bar_s = bar_q + 16,
+                   bar_p = bar_s + 16, bar_o = bar_p + 16, bar_end = bar_o + 16;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffBars + kBars * 8);
+    volatile uint32_t* dead = s_tmem + 1;
+    int* s_start = reinterpret_cast<int*>(s_tmem + 2);  // b, h, qt, skip of the share's first unit
+    Plan P;
+    P.units = reinterpret_cast<long long*>(smem + kOffUnits);
+    P.q0 = reinterpret_cast<int*>(smem + kOffSeq);
+    P.q = P.q0 + ECCO_MAX_BATCH;
+    P.base = P.q + ECCO_MAX_BATCH;
+    P.keys = P.base + ECCO_MAX_BATCH;
+    P.tile = P.keys + ECCO_MAX_BATCH;
+    P.batch = A.p.batch;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int window = A.w.window;
+
+    // ---- plan
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(bar_full + 8 * i, 1);
+            mbar_init(bar_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_q + 8 * i, 128);
+            mbar_init(bar_s + 8 * i, 1);
+            mbar_init(bar_p + 8 * i, 128);
+            mbar_init(bar_o + 8 * i, 1);
+        }
+        mbar_init(bar_end, 1);
+        *dead = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    for (int b = tid; b < P.batch; b += kAttnThreads) {
+        const Seq s = seq_of(A.p, A.w, b);
         int first, count;
-        seq_tiles(seq_of(A.p, A.w, b), A.w.window, first, count);
-        s_cu[b] = count;
-        s_first[b] = first;
+        seq_tiles(s, window, first, count);
+        P.q0[b] = s.q0;
+        P.q[b] = s.q;
+        P.base[b] = s.base;
+        P.keys[b] = s.keys;
+        P.tile[b] = count;
     }
     __syncthreads();
-    if (tid < 32) warp_prefix(s_cu, A.p.batch, tid);
+    for (int b = warp; b < P.batch; b += kAttnThreads / 32) {
+        const Seq s = P.seq(b);
+        const int n = (s.q * A.group + kRows - 1) / kRows;
+        long long u = 0;
+        for (int qt = lane; qt < n; qt += 32) u += max(1, span_of(s, A.group, window, qt).n);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+        if (lane == 0) P.units[b] = u * A.hn;
+    }
     __syncthreads();
-    const int tiles = s_cu[A.p.batch], heads = A.hn * A.group;
-    for (int b = 0; b < A.p.batch; ++b) {
-        const Seq s = seq_of(A.p, A.w, b);
-        const int64_t work = (int64_t)s.q * heads;
-        for (int64_t u = (int64_t)blockIdx.x * kWarps + (tid >> 5); u < work; u += (int64_t)gridDim.x * kWarps) {
-            const int i = (int)(u / heads), j = (int)(u - (int64_t)i * heads), h = j / A.group;
-            const int64_t row = s.q0 + i;
-            const int qh = A.h0 * A.group + j;
-            const uint16_t* q = A.q + row * A.q_token + qh * A.q_head + 4 * lane;
-            float qv[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
+    if (warp == 0) {
+        long long run = 0;
+        for (int i0 = 0; i0 < P.batch; i0 += 32) {
+            const int i = i0 + lane;
+            const long long x = i < P.batch ? P.units[i] : 0;
+            long long s = x;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) qv[k] = bf16_bits_to_f32(q[k]);
-            int lo, hi;
-            visible(s, A.w.window, i, i, lo, hi);
-            for (int t = lo; t < hi; ++t) {
-                const int64_t tile = (int64_t)h * tiles + s_cu[b] + t / kTile - s_first[b];
-                const uint8_t* kt = A.scratch + tile * kTileBytes;
-                const uint8_t* vt = kt + (int64_t)A.hn * tiles * kTileBytes;
-                const uint32_t at = tile_offset(t % kTile, lane >> 1) + (lane & 1) * 8;
-                const uint2 kw = *reinterpret_cast<const uint2*>(kt + at), vw = *reinterpret_cast<const uint2*>(vt + at);
-                float d = qv[0] * __uint_as_float(kw.x << 16) + qv[1] * __uint_as_float(kw.x & 0xffff0000u) +
-                          qv[2] * __uint_as_float(kw.y << 16) + qv[3] * __uint_as_float(kw.y & 0xffff0000u);
-#pragma unroll
-                for (int x = 16; x; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-                d *= A.scale;
-                const float mn = fmaxf(m, d), c = __expf(m - mn), p = __expf(d - mn);
-                m = mn;
-                l = l * c + p;
-                o[0] = o[0] * c + p * __uint_as_float(vw.x << 16);
-                o[1] = o[1] * c + p * __uint_as_float(vw.x & 0xffff0000u);
-                o[2] = o[2] * c + p * __uint_as_float(vw.y << 16);
-                o[3] = o[3] * c + p * __uint_as_float(vw.y & 0xffff0000u);
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, s, d);
+                if (lane >= d) s += t;
             }
-            const float inv = hi > lo ? 1.0f / l : 0.0f;
-            uint2 w;
-            w.x = pack_bf16x2(o[0] * inv, o[1] * inv);
-            w.y = pack_bf16x2(o[2] * inv, o[3] * inv);
-            *reinterpret_cast<uint2*>(A.out + row * A.out_token + qh * A.out_head + 4 * lane) = w;
-            if (A.lse && lane == 0)
-                A.lse[row * (int64_t)A.p.kv_heads * A.group + qh] = hi > lo ? m + logf(l) : -INFINITY;
+            if (i < P.batch) P.units[i] = run + s - x;
+            run += __shfl_sync(0xffffffffu, s, 31);
+        }
+        if (lane == 0) P.units[P.batch] = run;
+    } else if (warp == 1) {
+        warp_prefix(P.tile, P.batch, lane);
+    }
+    __syncthreads();
+    P.tiles = P.tile[P.batch];
+    const long long total = P.units[P.batch];
+    const long long shares = min((long long)gridDim.x, total);  // none of them empty
+    const bool works = blockIdx.x < shares;
+    const long long u0 = works ? total * blockIdx.x / shares : 0, u1 = works ? total * (blockIdx.x + 1) / shares : 0;
+    __syncthreads();
+    for (int b = tid; b < P.batch; b += kAttnThreads) {
+        int first, count;
+        seq_tiles(P.seq(b), window, first, count);
+        P.tile[b] -= first;
+    }
+    if (warp == 0 && u0 < u1) {  // the item of the share's first unit
+        int b = 0, top = P.batch - 1;
+        while (b < top) {
+            const int mid = (b + top + 1) >> 1;
+            if (P.units[mid] <= u0)
+                b = mid;
+            else
+                top = mid - 1;
+        }
+        const Seq s = P.seq(b);
+        const long long per_head = (P.units[b + 1] - P.units[b]) / A.hn;
+        long long rem = u0 - P.units[b];
+        const int h = (int)(rem / per_head);
+        rem -= h * per_head;
+        const int n = (s.q * A.group + kRows - 1) / kRows;
+        for (int q0 = 0; q0 < n; q0 += 32) {
+            const int qt = q0 + lane;
+            const int x = qt < n ? max(1, span_of(s, A.group, window, qt).n) : 0;
+            long long sum = x;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += t;
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, sum > rem);
+            if (m) {
+                if (lane == __ffs(m) - 1) {
+                    s_start[0] = b;
+                    s_start[1] = h;
+                    s_start[2] = qt;
+                    s_start[3] = (int)(rem - (sum - x));
+                }
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, sum, 31);
         }
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    Walk W{P, A.group, window, A.hn, u0, u1, s_start[0], s_start[1], s_start[2], s_start[3]};
+    const int64_t v_offset = (int64_t)A.hn * P.tiles * kTileBytes;
+
+    if (warp == 9) {
+        // ---- copies: K_0 V_0 K_1 V_1 ... of every part
+        if (lane == 0) {
+            Part x;
+            uint32_t n = 0;
+            bool ok = true;
+            while (ok && W.next(x)) {
+                const uint8_t* src = A.scratch + ((int64_t)x.h * P.tiles + P.tile[x.b] + x.t0) * kTileBytes;
+                for (int j = 0; j < 2 * x.n; ++j, ++n) {
+                    const uint32_t st = n % kStages, use = n / kStages;
+                    if (use > 0 && !(ok = mbar_wait(bar_empty + 8 * st, (use - 1) & 1, dead, A.flag))) break;
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar_full + 8 * st), "r"(kTileBytes)
+                                 : "memory");
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                            smem_u32(smem + kOffRing) + st * kTileBytes),
+                        "l"(src + (int64_t)(j >> 1) * kTileBytes + ((j & 1) ? v_offset : 0)), "r"(kTileBytes), "r"(bar_full + 8 * st)
+                        : "memory");
+                }
+            }
+            // every copy has landed before the CTA ends (they have, unless it gave up)
+            for (uint32_t k = n > kStages ? n - kStages : 0; k < n; ++k) {
+                uint32_t zero = 0u;
+                mbar_wait(bar_full + 8 * (k % kStages), (k / kStages) & 1, &zero, nullptr);
+            }
+        }
+    } else if (warp == 8) {
+        // ---- products
+        if (lane == 0) {
+            Part x;
+            uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+            bool ok = true;
+            auto wait = [&](uint32_t bar, uint32_t count) {
+                if (ok) ok = mbar_wait(bar, count & 1, dead, A.flag);
+                tc_fence_after();
+                return ok;
+            };
+            auto full = [&](uint32_t k) { return wait(bar_full + 8 * (k % kStages), k / kStages); };
+            const uint32_t ring = smem_u32(smem + kOffRing), qs = smem_u32(smem);
+            auto score = [&](int i, uint32_t k) {
+                const uint64_t a = sw128_desc(qs + i * kTileBytes), b = sw128_desc(ring + (k % kStages) * kTileBytes);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    const uint64_t o = (uint64_t)(((t >> 2) * (kTileBytes / 2) + (t & 3) * 32) >> 4);
+                    mma_ss(tmem + 128 * i, a + o, b + o, t > 0);
+                }
+                mma_commit(bar_s + 8 * i);
+            };
+            while (ok && W.next(x)) {
+                if (x.n == 0) continue;
+                const int tiles = x.rows > 128 ? 2 : 1;
+                for (int i = 0; i < tiles; ++i) {
+                    if (!wait(bar_q + 8 * i, nq[i]++)) break;
+                    if (i == 0 && !full(n)) break;
+                    score(i, n);
+                }
+                if (!ok) break;
+                mma_commit(bar_empty + 8 * (n % kStages));
+                for (int j = 0; j < x.n && ok; ++j) {
+                    const uint32_t v = n + 2 * j + 1, k = v + 1;
+                    for (int i = 0; i < tiles; ++i) {
+                        if (!wait(bar_p + 8 * i, np[i]++)) break;
+                        if (i == 0 && !full(v)) break;
+                        const uint64_t b = sw128_desc(ring + (v % kStages) * kTileBytes);
+#pragma unroll
+                        for (int t = 0; t < 8; ++t)
+                            mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, b + (uint64_t)(t * 2048 >> 4), (j > 0 || t > 0) ? 1u : 0u);
+                        mma_commit(bar_o + 8 * i);
+                        if (i == tiles - 1) mma_commit(bar_empty + 8 * (v % kStages));
+                        if (j + 1 < x.n) {
+                            if (i == 0 && !full(k)) break;
+                            score(i, k);
+                            if (i == tiles - 1) mma_commit(bar_empty + 8 * (k % kStages));
+                        }
+                    }
+                }
+                n += 2 * x.n;
+            }
+            // every product issued is done before the tensor memory is freed
+            uint32_t zero = 0u;
+            mma_commit(bar_end);
+            mbar_wait(bar_end, 0u, &zero, nullptr);
+        }
+    } else if (warp < 8) {
+        // ---- softmax: thread = row `row` of tile i
+        const int i = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + 128 * i, to = tmem + lanes + 256 + 128 * i;
+        uint8_t* qs = smem + i * kTileBytes;
+        const uint32_t flip = A.scale < 0.0f ? 0x80008000u : 0u;       // a negative scale turns Q's signs
+        const float c = fmaxf(fabsf(A.scale) * 1.44269504f, 1e-30f);  // 0: weights of 1, and masked scores stay -inf
+        uint32_t ns = 0, no = 0;
+        bool ok = true, more;
+        Part x, y;
+        auto load_q = [&](const Part& z) {  // this thread's row of Q, zeros behind the item's rows
+            const int r = i * 128 + row;
+            uint4 v[16];
+            if (r < z.rows) {
+                const int g = z.qt * kRows + r, tok = P.q0[z.b] + g / A.group;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    A.q + (int64_t)tok * A.q_token + (int64_t)((A.h0 + z.h) * A.group + g % A.group) * A.q_head);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    v[k] = src[k];
+                    v[k] = make_uint4(v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(qs + tile_offset(row, k)) = v[k];
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(bar_q + 8 * i);
+        };
+        auto wait = [&](uint32_t bar, uint32_t count) {  // the whole warp: tensor-memory instructions follow
+            if (ok) ok = mbar_wait(bar, count & 1, dead, A.flag);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+        };
+        auto active = [&](const Part& z) { return z.n > 0 && z.rows > 128 * i; };
+        more = W.next(x);
+        if (more && active(x)) load_q(x);
+        while (more) {
+            const bool has = W.next(y);
+            const int r = i * 128 + row, g = x.qt * kRows + r;
+            const Seq s = P.seq(x.b);
+            const bool real = r < x.rows;
+            const int tok = real ? g / A.group : 0;
+            int klo, khi;  // keys that this row sees
+            visible(s, window, tok, tok, klo, khi);
+            if (!real) klo = khi = 0;
+            // and those that every row of this tile sees: no mask for key tiles inside them
+            int alo, ahi;
+            {
+                const int last = min(x.qt * kRows + 128 * i + 127, x.qt * kRows + x.rows - 1) / A.group;
+                const int first = (x.qt * kRows + 128 * i) / A.group;
+                ahi = min(s.keys, s.base + first + 1);
+                alo = window > 0 ? max(0, s.base + last - window + 1) : 0;
+            }
+            float m = -INFINITY, l = 0.0f;
+            if (active(x)) {
+                for (int j = 0; j < x.n; ++j) {
+                    const int k0 = (x.t0 + j) * kTile;
+                    wait(bar_s + 8 * i, ns++);
+                    uint32_t v[128];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, v + 32 * k);
+                    tmem_wait_ld();
+                    if (k0 < alo || k0 + kTile > ahi) {
+                        const int lo = klo - k0, hi = khi - k0;
+#pragma unroll
+                        for (int k = 0; k < 128; ++k)
+                            if (k < lo || k >= hi) v[k] = 0xff800000u;
+                    }
+                    float top[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(v[k]);
+#pragma unroll
+                    for (int k = 4; k < 128; k += 4)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) top[t] = fmaxf(top[t], __uint_as_float(v[k + t]));
+                    const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    if (j == 0) {
+                        m = mt;
+                    } else if (__any_sync(0xffffffffu, (mt - m) * c > 8.0f)) {
+                        const float mn = fmaxf(m, mt), f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
+                        m = mn;
+                        l *= f;
+                        wait(bar_o + 8 * i, no - 1);
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t o[32];
+                            tmem_ld32(to + 32 * k, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
+                            tmem_st32(to + 32 * k, o);
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) {
+                        const float e = ex2(fmaf(__uint_as_float(v[k]), c, -mc));
+                        sum[k & 3] += e;
+                        v[k] = __float_as_uint(e);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            pk[k] = pack_bf16x2(__uint_as_float(v[64 * hf + 2 * k]), __uint_as_float(v[64 * hf + 2 * k + 1]));
+                        tmem_st32(ts + 32 * hf, pk);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(bar_p + 8 * i);
+                    ++no;
+                }
+            }
+            if (has && active(y)) load_q(y);  // the scores that read Q are done
+            if (x.rows > 128 * i) {
+                if (x.n > 0) wait(bar_o + 8 * i, no - 1);
+                const bool whole = x.begins && x.ends;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (x.begins ? 1 : 0);
+                const int64_t at = (int64_t)s.q0 + tok;
+                const int qh = (A.h0 + x.h) * A.group + g % A.group;
+                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    if (x.n > 0) {
+                        tmem_ld32(to + 32 * k, o);
+                        tmem_wait_ld();
+                    } else {  // the row sees no key
+#pragma unroll
+                        for (int t = 0; t < 32; ++t) o[t] = 0u;
+                    }
+                    if (!ok || !real) {
+                    } else if (whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(A.out + at * A.out_token + (int64_t)qh * A.out_head) + 4 * k;
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack_bf16x2(__uint_as_float(o[8 * t + 2 * e]) * inv, __uint_as_float(o[8 * t + 2 * e + 1]) * inv);
+                            dst[t] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(A.part_o) + (slot * 32 + 8 * k) * A.slot_rows + r;
+#pragma unroll
+                        for (int t = 0; t < 8; ++t)
+                            dst[t * A.slot_rows] = make_uint4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
+                    }
+                }
+                if (ok && real) {
+                    if (whole) {
+                        if (A.lse)
+                            A.lse[at * A.p.kv_heads * A.group + qh] =
+                                l == 0.0f ? -INFINITY : fmaf(m, c * 0.69314718f, logf(l));
+                    } else {
+                        A.part_ml[(slot * 2) * A.slot_rows + r] = m == -INFINITY ? -INFINITY : m * c;
+                        A.part_ml[(slot * 2 + 1) * A.slot_rows + r] = l;
+                    }
+                }
+                tc_fence_before();  // O is read before the next part's first product is allowed in
+            }
+            if (tid == 0 && x.begins && !x.ends) {
+                const long long last = x.at + x.units - 1;
+                A.part_item[blockIdx.x] = make_int4(x.b, x.h, x.qt, (int)(((last + 1) * shares - 1) / total));
+            }
+            if (tid == 0 && !has && (!x.begins || x.ends)) A.part_item[blockIdx.x] = make_int4(0, -1, 0, 0);
+            x = y;
+            more = has;
+        }
+        __syncwarp();
+        if (tid == 0 && !works) A.part_item[blockIdx.x] = make_int4(0, -1, 0, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// Joins the parts of the items that were cut: block (c, piece) the item that
+// CTA c began and left unfinished.  A thread joins 4 values of a row.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnArgs A)
+{
+    const int4 it = A.part_item[blockIdx.x];
+    if (it.y < 0) return;
+    const Seq s = seq_of(A.p, A.w, it.x);
+    const int rows = min(kRows, s.q * A.group - it.z * kRows);
+    const int at = blockIdx.y * kJoinThreads + threadIdx.x;
+    if (at >= rows * 32) return;
+    const int r = at % rows, c4 = at / rows;
+    const int c0 = blockIdx.x, c1 = it.w;
+    auto slot = [&](int c) -> int64_t { return 2 * (int64_t)c + (c == c0 ? 1 : 0); };
+    float m = -INFINITY, l = 0.0f;
+    for (int c = c0; c <= c1; ++c) m = fmaxf(m, A.part_ml[slot(c) * 2 * A.slot_rows + r]);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int c = c0; c <= c1; ++c) {
+        const float mc = A.part_ml[slot(c) * 2 * A.slot_rows + r];
+        const float f = mc == -INFINITY ? 0.0f : exp2f(mc - m);
+        l += f * A.part_ml[(slot(c) * 2 + 1) * A.slot_rows + r];
+        const float4 v = reinterpret_cast<const float4*>(A.part_o)[(slot(c) * 32 + c4) * A.slot_rows + r];
+        o.x += f * v.x;
+        o.y += f * v.y;
+        o.z += f * v.z;
+        o.w += f * v.w;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int g = it.z * kRows + r, qh = (A.h0 + it.y) * A.group + g % A.group;
+    const int64_t row = (int64_t)s.q0 + g / A.group;
+    uint2 w;
+    w.x = pack_bf16x2(o.x * inv, o.y * inv);
+    w.y = pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(A.out + row * A.out_token + (int64_t)qh * A.out_head + 4 * c4) = w;
+    if (A.lse && c4 == 0)
+        A.lse[row * A.p.kv_heads * A.group + qh] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
 }
 
 // Heads of a round: as many as keep the scratch within kRoundBytes, at least one.
@@ -303,30 +907,57 @@ int round_heads(int batch, int kv_heads, int max_kv)
     return (int)std::max<int64_t>(1, std::min<int64_t>(kv_heads, per_head ? kRoundBytes / per_head : kv_heads));
 }
 
+// Workspace: items cut [kMaxCtas], (max, sum) and O of the slots, the scratch.
+struct Layout {
+    size_t ml, o, scratch, bytes;
+    int slot_rows;
+};
+
+Layout layout(int batch, int kv_heads, int group, int max_q, int max_kv)
+{
+    const auto up = [](size_t n) { return (n + 1023) / 1024 * 1024; };
+    Layout L;
+    L.slot_rows = (int)std::min<int64_t>(kRows, std::max<int64_t>(1, (int64_t)max_q * group));
+    L.ml = up(kMaxCtas * sizeof(int4));
+    L.o = L.ml + up((size_t)2 * kMaxCtas * 2 * L.slot_rows * sizeof(float));
+    L.scratch = L.o + up((size_t)2 * kMaxCtas * 32 * L.slot_rows * sizeof(float4));
+    const int64_t tiles = (int64_t)batch * ((max_kv + kTile - 1) / kTile);
+    L.bytes = L.scratch + (size_t)(2 * round_heads(batch, kv_heads, max_kv) * tiles * kTileBytes) + 1024;
+    return L;
+}
+
 }  // namespace
 
 size_t paged_attention_bytes(int batch, int kv_heads, int group, int max_q, int max_kv)
 {
-    const int64_t tiles = (int64_t)batch * ((max_kv + kTile - 1) / kTile);
-    return (size_t)(2 * round_heads(batch, kv_heads, max_kv) * tiles * kTileBytes) + 1024;
+    return layout(batch, kv_heads, group, max_q, max_kv).bytes;
 }
+
+cudaError_t paged_timeouts(unsigned int* n) { return cudaMemcpyFromSymbol(n, g_timeouts, sizeof(*n)); }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* workspace, cudaStream_t s)
 {
-    static std::atomic<uint64_t> configured{0};
-    cudaError_t e = set_max_smem_once(configured, (const void*)paged_decode_kernel, kDecSmem);
+    static std::atomic<uint64_t> configured[2]{};
+    cudaError_t e = set_max_smem_once(configured[0], (const void*)paged_decode_kernel, kDecSmem);
+    if (e == cudaSuccess) e = set_max_smem_once(configured[1], (const void*)paged_attention_kernel, kAttnSmem);
     if (e != cudaSuccess) return e;
-    uint8_t* scratch = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 1023) / 1024 * 1024);
+    const Layout L = layout(a.p.batch, a.p.kv_heads, a.group, a.max_q, a.max_kv);
+    uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 1023) / 1024 * 1024);
+    uint8_t* scratch = ws + L.scratch;
     const int hn = round_heads(a.p.batch, a.p.kv_heads, a.max_kv);
+    const int ctas = std::min(device_sm_count(), kMaxCtas);
     const Bounds w{a.tokens, a.max_q, a.max_kv, a.window};
     for (int h0 = 0; h0 < a.p.kv_heads; h0 += hn) {
         const int n = std::min(hn, a.p.kv_heads - h0);
         const StageArgs st{a.p, w, {a.tb[0], a.tb[1]}, {a.pages[0], a.pages[1]}, scratch, h0, n};
         paged_decode_kernel<<<device_sm_count(), kDecThreads, kDecSmem, s>>>(st);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        const AttnArgs at{a.p, w, scratch, a.q, a.out, a.lse, a.q_token, a.q_head, a.out_token, a.out_head,
-                          a.group, h0, n, a.scale};
-        paged_attention_kernel<<<device_sm_count() * 8, kWarps * 32, 0, s>>>(at);
+        const AttnArgs at{a.p, w, scratch, a.q, a.out, a.lse, a.q_token, a.q_head, a.out_token, a.out_head, a.group, h0, n,
+                          a.scale, reinterpret_cast<float*>(ws + L.o), reinterpret_cast<float*>(ws + L.ml),
+                          reinterpret_cast<int4*>(ws), L.slot_rows, timeout_flag()};
+        paged_attention_kernel<<<ctas, kAttnThreads, kAttnSmem, s>>>(at);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        paged_join_kernel<<<dim3(ctas, (L.slot_rows * 32 + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, s>>>(at);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     return cudaSuccess;

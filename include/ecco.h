@@ -447,13 +447,14 @@ int ecco_learn_tables(const uint16_t* sample_bf16, int64_t n_groups, int group, 
  * n > 2^max_len. */
 int ecco_huffman_lengths(const double* weights, int n, int max_len, uint8_t* lengths_out);
 
-/* Number of bounded device-side waits (tensor-core decode+GEMV pipeline) that
- * gave up since the library was loaded on the current device; 0 in normal
- * operation.  A CTA whose wait gives up stops issuing tensor-core work, adds
- * nothing to y and returns instead of hanging, so that launch's y is
- * incomplete.  Because launches are asynchronous, the failure is reported
+/* Number of bounded device-side waits (tensor-core decode+GEMV pipeline, paged
+ * attention) that gave up since the library was loaded on the current device; 0
+ * in normal operation.  A CTA whose wait gives up stops issuing tensor-core work,
+ * adds nothing to y (writes no more of the attention's out) and returns instead
+ * of hanging, so that launch's result is incomplete.  Because launches are asynchronous, the failure is reported
  * like CUDA's own asynchronous errors: it raises a host-visible flag, and
- * every later ecco_decode_gemv call with batch > 4 returns ECCO_ERR_TIMEOUT
+ * every later ecco_decode_gemv call with batch > 4 and every later
+ * ecco_paged_attention call returns ECCO_ERR_TIMEOUT
  * (enqueuing nothing) until this function is called, which reads the count
  * and clears the flag.  Blocking (reads device memory). */
 #define ECCO_ERR_TIMEOUT (-8) /* a bounded device wait gave up in an earlier launch */
