@@ -226,20 +226,23 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
 // ------------------------------------------------------------ attention
 // Persistent kernel, one CTA an SM.  An item is (sequence, KV head, 256 rows),
 // a row being (new token, query head of the group), so that a tile of keys
-// serves every query head that shares it.  Items cost as many units as the
-// 128-key tiles their rows see (at least one); the units of all items, in one
-// line, are cut into equal shares, so a CTA's share may begin and end inside
-// items: such parts leave (O, max, sum) in the workspace, and a second kernel
-// joins them.  The cut needs no rule for the number of splits, and prompts
-// with triangular costs, ragged batches and single tokens over a long cache
-// all fill the SMs alike.
+// serves every query head that shares it.  An item costs, for each 128-key
+// tile that its rows see, two units, or one if it has at most 128 rows; the
+// units of all items, in one line, are cut into equal shares, so a CTA's share
+// may begin and end inside items: such parts leave (O, max, sum) in the
+// workspace, and a second kernel joins them.  The cut needs no rule for the
+// number of splits, and prompts with triangular costs, ragged batches and
+// single tokens over a long cache all fill the SMs alike.
 //
-// Inside an item, two row tiles of 128 alternate on the tensor cores:
+// Inside an item, two engines alternate on the tensor cores:
 //   S_i = Q_i K_j^T   (128 x 128 x 128, both from shared memory, into TMEM)
 //   P_i = exp2(c S_i - c m), one thread a row, back to TMEM as bf16 over S_i
 //   O_i += P_i V_j    (P from TMEM, V as it lies: rows of keys, N-major)
-// Warps 0-3 and 4-7 hold the rows of tile 0 and 1, lane = TMEM lane; warp 8
-// issues the products, warp 9 the copies (a tile is one 32 KB bulk copy).
+// With more than 128 rows ("wide") engine i has rows 128 i .. of every tile;
+// with fewer ("thin") both have the same rows, engine i the key tiles i, i + 2,
+// .. of the part, and engine 0 joins the two.  Warps 0-3 and 4-7 are the
+// engines' softmax, a thread a row = a TMEM lane; warp 8 issues the products,
+// warp 9 the copies (a tile is one 32 KB bulk copy).
 // The maximum m is only moved, and O rescaled, when a row's new maximum is
 // above it by more than 2^8: until then the weights stay below 2^8 and sum and
 // products are as exact as with the true maximum.
@@ -266,13 +269,18 @@ constexpr int kRows = 256;               // rows of an item
 constexpr int kAttnThreads = 384;
 constexpr int kStages = 4;               // K and V tiles in flight
 constexpr int kMaxCtas = 160;            // shares (and twice as many slots) at most
-constexpr int kBars = 2 * kStages + 9;
+constexpr int kBars = 2 * kStages + 13;
 constexpr size_t kOffRing = 2 * kTileBytes;
 constexpr size_t kOffBars = kOffRing + (size_t)kStages * kTileBytes;
-constexpr size_t kOffUnits = kOffBars + kBars * 8 + 56;
-constexpr size_t kOffSeq = kOffUnits + (ECCO_MAX_BATCH + 1) * 8 + 8;
+constexpr size_t kOffUnits = kOffBars + kBars * 8 + 24 + 1024;
+constexpr size_t kOffSeq = (kOffUnits + (ECCO_MAX_BATCH + 1) * 8 + 15) / 16 * 16;
 constexpr size_t kAttnSmem = 1024 + kOffSeq + sizeof(int) * (5 * ECCO_MAX_BATCH + 1);
 constexpr uint32_t kSpinLimit = 1u << 20;
+// Registers a thread: 384 threads start with 168 (65,536 / 384, in eights);
+// the softmax warps take 216, the other warpgroup gives up 96 of its 168:
+// 256 * 216 + 128 * 72 = 64,512 = 384 * 168.
+constexpr int kSoftRegs = 216, kIssueRegs = 72;
+static_assert(256 * kSoftRegs + 128 * kIssueRegs <= kAttnThreads * 168, "more registers than the block was launched with");
 
 __device__ unsigned int g_timeouts = 0;
 
@@ -310,10 +318,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(1000u)
+            : "r"(bar), "r"(parity)
             : "memory");
         if (done) return true;
         if (*dead) return false;
@@ -327,29 +335,49 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return false;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate)
+// The issuing warp runs as a whole (`leader` is true in one lane), so that the
+// operands stay in uniform registers: issued from a branch of one lane, the
+// eight products of a tile took 600 cycles to issue, more than they run.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate, uint32_t leader)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(kIdescQK), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(kIdescQK), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t accumulate, uint32_t leader)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(kIdescPV), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(kIdescPV), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint32_t bar)
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint32_t leader)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
 }
 
 #define ECCO_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
@@ -365,12 +393,19 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* v)
         : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* v)
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* v)
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::ECCO_I8(v, 0),
-        ECCO_I8(v, 8), ECCO_I8(v, 16), ECCO_I8(v, 24), "r"(addr)
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : ECCO_R8(v, 0), ECCO_R8(v, 8)
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::ECCO_I8(v, 0),
+        ECCO_I8(v, 8), "r"(addr)
         : "memory");
 }
 
@@ -384,6 +419,47 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The weights 2^(c s - mc) of 32 scores, packed as bf16 into w, their sum added
+// to `sum`.
+__device__ __forceinline__ void weights(const uint32_t* v, uint64_t c2, uint64_t mc2, uint32_t* w, uint64_t (&sum)[2])
+{
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+        float a, b;
+        unpair(fma2(pair(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, mc2), a, b);
+        a = ex2(a);
+        b = ex2(b);
+        sum[k & 1] = add2(sum[k & 1], pair(a, b));
+        w[k] = pack_bf16x2(a, b);
+    }
 }
 
 // The tiles [t0, t0 + n) that rows 256 qt .. of the sequence see, and its rows.
@@ -403,31 +479,44 @@ __device__ __forceinline__ Span span_of(const Seq& s, int group, int window, int
     return r;
 }
 
-struct Plan {  // in shared memory
-    long long* units;  // [batch + 1] units before sequence b, over the round's heads
-    int *q0, *q, *base, *keys, *tile;  // tile: scratch tile of (head 0, key tile 0) of sequence b
+struct Plan {  // in shared memory, at `at`
+    uint8_t* at;
     int batch, tiles;
-    __device__ __forceinline__ Seq seq(int b) const { return Seq{q0[b], q[b], base[b], keys[b]}; }
+    __device__ __forceinline__ long long* units() const { return reinterpret_cast<long long*>(at + kOffUnits); }  // [batch + 1] units before sequence b, over the round's heads
+    __device__ __forceinline__ int4* seqs() const { return reinterpret_cast<int4*>(at + kOffSeq); }
+    __device__ __forceinline__ int* tile() const { return reinterpret_cast<int*>(at + kOffSeq + 16 * ECCO_MAX_BATCH); }  // scratch tile of (head 0, key tile 0) of sequence b
+    __device__ __forceinline__ Seq seq(int b) const
+    {
+        const int4 v = seqs()[b];
+        return Seq{v.x, v.y, v.z, v.w};
+    }
 };
+
+// Units that a key tile of the span costs.
+__device__ __forceinline__ int tile_cost(const Span& r) { return r.rows > 128 ? 2 : 1; }
 
 // One part of an item: key tiles [t0, t0 + n) of its rows.
 struct Part {
     int b, h, qt, rows, t0, n;
     bool begins, ends;  // the item's first / last tiles are among them
-    long long at;       // the item's first unit
-    int units;          // of the item
+    long long last;     // the item's last unit
+    __device__ __forceinline__ bool thin() const { return rows <= 128; }
+    __device__ __forceinline__ int row0(int i) const { return thin() ? 0 : 128 * i; }  // of engine i's tile
+    __device__ __forceinline__ int tiles(int i) const { return thin() ? (n + 1 - i) >> 1 : n; }
+    __device__ __forceinline__ bool active(int i) const { return tiles(i) > 0; }
 };
 
-// Walks a share's parts.  Every warp runs its own copy.
+// Walks a share's parts.  Every warp runs its own copy.  A tile belongs to the
+// share that holds its last unit.
 struct Walk {
     const Plan& P;
     int group, window, hn;
-    long long at, stop;  // next unit, end of the share
-    int b, h, qt, skip;  // item of unit `at`, units of it before `at`
+    long long item, stop;  // first unit of the item, end of the share
+    int b, h, qt, skip;    // the item, and its tiles before the share
 
     __device__ __forceinline__ bool next(Part& x)
     {
-        if (at >= stop) return false;
+        if (item >= stop) return false;
         Seq s = P.seq(b);
         while (qt * kRows >= s.q * group) {  // the sequence's rows are done: its next head, or the next sequence with rows
             qt = 0;
@@ -436,19 +525,19 @@ struct Walk {
             s = P.seq(++b);
         }
         const Span r = span_of(s, group, window, qt);
-        const int units = max(1, r.n);
-        const int take = (int)min((long long)(units - skip), stop - at);
+        const int units = max(1, r.n), cost = tile_cost(r);
+        const int until = (int)min((long long)units, (stop - item) / cost);
+        if (until <= skip) return false;
         x.b = b;
         x.h = h;
         x.qt = qt;
         x.rows = r.rows;
         x.t0 = r.t0 + skip;
-        x.n = min(take, r.n - skip);
+        x.n = min(until, r.n) - skip;
         x.begins = skip == 0;
-        x.ends = skip + take == units;
-        x.at = at - skip;
-        x.units = units;
-        at += take;
+        x.ends = until == units;
+        x.last = item + (long long)units * cost - 1;
+        item += (long long)units * cost;
         skip = 0;
         ++qt;
         return true;
@@ -458,20 +547,17 @@ struct Walk {
 __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const __grid_constant__ AttnArgs A)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ long long s_item;  // first unit of the share's first item
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
     const uint32_t bars = smem_u32(smem + kOffBars);
     const uint32_t bar_full = bars, bar_empty = bars + 8 * kStages, bar_q = bars + 16 * kStages, bar_s = bar_q + 16,
-                   bar_p = bar_s + 16, bar_o = bar_p + 16, bar_end = bar_o + 16;
+                   bar_p = bar_s + 16, bar_o = bar_p + 32, bar_x = bar_o + 16, bar_end = bar_x + 16;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffBars + kBars * 8);
     volatile uint32_t* dead = s_tmem + 1;
     int* s_start = reinterpret_cast<int*>(s_tmem + 2);  // b, h, qt, skip of the share's first unit
+    float* s_ml = reinterpret_cast<float*>(s_start + 4);  // engine 1's maxima and sums of a thin part, for engine 0
     Plan P;
-    P.units = reinterpret_cast<long long*>(smem + kOffUnits);
-    P.q0 = reinterpret_cast<int*>(smem + kOffSeq);
-    P.q = P.q0 + ECCO_MAX_BATCH;
-    P.base = P.q + ECCO_MAX_BATCH;
-    P.keys = P.base + ECCO_MAX_BATCH;
-    P.tile = P.keys + ECCO_MAX_BATCH;
+    P.at = smem;
     P.batch = A.p.batch;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int window = A.w.window;
@@ -486,7 +572,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
             mbar_init(bar_q + 8 * i, 128);
             mbar_init(bar_s + 8 * i, 1);
             mbar_init(bar_p + 8 * i, 128);
+            mbar_init(bar_p + 16 + 8 * i, 128);
             mbar_init(bar_o + 8 * i, 1);
+            mbar_init(bar_x + 8 * i, 128);
         }
         mbar_init(bar_end, 1);
         *dead = 0u;
@@ -501,71 +589,73 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
         const Seq s = seq_of(A.p, A.w, b);
         int first, count;
         seq_tiles(s, window, first, count);
-        P.q0[b] = s.q0;
-        P.q[b] = s.q;
-        P.base[b] = s.base;
-        P.keys[b] = s.keys;
-        P.tile[b] = count;
+        P.seqs()[b] = make_int4(s.q0, s.q, s.base, s.keys);
+        P.tile()[b] = count;
     }
     __syncthreads();
     for (int b = warp; b < P.batch; b += kAttnThreads / 32) {
         const Seq s = P.seq(b);
         const int n = (s.q * A.group + kRows - 1) / kRows;
         long long u = 0;
-        for (int qt = lane; qt < n; qt += 32) u += max(1, span_of(s, A.group, window, qt).n);
+        for (int qt = lane; qt < n; qt += 32) {
+            const Span r = span_of(s, A.group, window, qt);
+            u += max(1, r.n) * tile_cost(r);
+        }
 #pragma unroll
         for (int d = 16; d; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
-        if (lane == 0) P.units[b] = u * A.hn;
+        if (lane == 0) P.units()[b] = u * A.hn;
     }
     __syncthreads();
     if (warp == 0) {
         long long run = 0;
         for (int i0 = 0; i0 < P.batch; i0 += 32) {
             const int i = i0 + lane;
-            const long long x = i < P.batch ? P.units[i] : 0;
+            const long long x = i < P.batch ? P.units()[i] : 0;
             long long s = x;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const long long t = __shfl_up_sync(0xffffffffu, s, d);
                 if (lane >= d) s += t;
             }
-            if (i < P.batch) P.units[i] = run + s - x;
+            if (i < P.batch) P.units()[i] = run + s - x;
             run += __shfl_sync(0xffffffffu, s, 31);
         }
-        if (lane == 0) P.units[P.batch] = run;
+        if (lane == 0) P.units()[P.batch] = run;
     } else if (warp == 1) {
-        warp_prefix(P.tile, P.batch, lane);
+        warp_prefix(P.tile(), P.batch, lane);
     }
     __syncthreads();
-    P.tiles = P.tile[P.batch];
-    const long long total = P.units[P.batch];
-    const long long shares = min((long long)gridDim.x, total);  // none of them empty
-    const bool works = blockIdx.x < shares;
+    P.tiles = P.tile()[P.batch];
+    const long long total = P.units()[P.batch];
+    const long long shares = min((long long)gridDim.x, max(1ll, total / 2));  // of two units at least: each holds a tile's last
+    const bool works = total > 0 && blockIdx.x < shares;
     const long long u0 = works ? total * blockIdx.x / shares : 0, u1 = works ? total * (blockIdx.x + 1) / shares : 0;
     __syncthreads();
     for (int b = tid; b < P.batch; b += kAttnThreads) {
         int first, count;
         seq_tiles(P.seq(b), window, first, count);
-        P.tile[b] -= first;
+        P.tile()[b] -= first;
     }
     if (warp == 0 && u0 < u1) {  // the item of the share's first unit
         int b = 0, top = P.batch - 1;
         while (b < top) {
             const int mid = (b + top + 1) >> 1;
-            if (P.units[mid] <= u0)
+            if (P.units()[mid] <= u0)
                 b = mid;
             else
                 top = mid - 1;
         }
         const Seq s = P.seq(b);
-        const long long per_head = (P.units[b + 1] - P.units[b]) / A.hn;
-        long long rem = u0 - P.units[b];
+        const long long per_head = (P.units()[b + 1] - P.units()[b]) / A.hn;
+        long long rem = u0 - P.units()[b];
         const int h = (int)(rem / per_head);
         rem -= h * per_head;
         const int n = (s.q * A.group + kRows - 1) / kRows;
         for (int q0 = 0; q0 < n; q0 += 32) {
             const int qt = q0 + lane;
-            const int x = qt < n ? max(1, span_of(s, A.group, window, qt).n) : 0;
+            Span r{0, 0, 0};
+            if (qt < n) r = span_of(s, A.group, window, qt);
+            const int x = qt < n ? max(1, r.n) * tile_cost(r) : 0;
             long long sum = x;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -578,7 +668,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                     s_start[0] = b;
                     s_start[1] = h;
                     s_start[2] = qt;
-                    s_start[3] = (int)(rem - (sum - x));
+                    s_start[3] = (int)(rem - (sum - x)) / tile_cost(r);
+                    s_item = u0 - (rem - (sum - x));
                 }
                 break;
             }
@@ -589,27 +680,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    Walk W{P, A.group, window, A.hn, u0, u1, s_start[0], s_start[1], s_start[2], s_start[3]};
+    Walk W{P, A.group, window, A.hn, works ? s_item : 0, u1, s_start[0], s_start[1], s_start[2], s_start[3]};
     const int64_t v_offset = (int64_t)A.hn * P.tiles * kTileBytes;
 
-    if (warp == 9) {
-        // ---- copies: K_0 V_0 K_1 V_1 ... of every part
-        if (lane == 0) {
+    // The ring's tiles, in the order in which the products take them: wide parts
+    // K_0 V_0 K_1 V_1 .., thin ones K_0 K_1 V_0 K_2 V_1 K_3 ..
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == 9 && lane == 0) {
+            // ---- copies
             Part x;
             uint32_t n = 0;
             bool ok = true;
             while (ok && W.next(x)) {
-                const uint8_t* src = A.scratch + ((int64_t)x.h * P.tiles + P.tile[x.b] + x.t0) * kTileBytes;
-                for (int j = 0; j < 2 * x.n; ++j, ++n) {
+                const uint8_t* src = A.scratch + ((int64_t)x.h * P.tiles + P.tile()[x.b] + x.t0) * kTileBytes;
+                auto copy = [&](int j, bool v) {
                     const uint32_t st = n % kStages, use = n / kStages;
-                    if (use > 0 && !(ok = mbar_wait(bar_empty + 8 * st, (use - 1) & 1, dead, A.flag))) break;
+                    if (!ok || (use > 0 && !(ok = mbar_wait(bar_empty + 8 * st, (use - 1) & 1, dead, A.flag)))) return;
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar_full + 8 * st), "r"(kTileBytes)
                                  : "memory");
                     asm volatile(
                         "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                             smem_u32(smem + kOffRing) + st * kTileBytes),
-                        "l"(src + (int64_t)(j >> 1) * kTileBytes + ((j & 1) ? v_offset : 0)), "r"(kTileBytes), "r"(bar_full + 8 * st)
+                        "l"(src + (int64_t)j * kTileBytes + (v ? v_offset : 0)), "r"(kTileBytes), "r"(bar_full + 8 * st)
                         : "memory");
+                    ++n;
+                };
+                const int ahead = x.thin() ? 2 : 1;
+                for (int j = 0; j < min(ahead, x.n); ++j) copy(j, false);
+                for (int j = 0; j < x.n && ok; ++j) {
+                    copy(j, true);
+                    if (j + ahead < x.n) copy(j + ahead, false);
                 }
             }
             // every copy has landed before the CTA ends (they have, unless it gave up)
@@ -618,53 +719,87 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                 mbar_wait(bar_full + 8 * (k % kStages), (k / kStages) & 1, &zero, nullptr);
             }
         }
-    } else if (warp == 8) {
-        // ---- products
-        if (lane == 0) {
+        if (warp == 8) {
+            // ---- products (the whole warp)
+            const uint32_t leader = elect_one();
             Part x;
             uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};
             bool ok = true;
+            const uint32_t ring = smem_u32(smem + kOffRing), qs = smem_u32(smem);
             auto wait = [&](uint32_t bar, uint32_t count) {
                 if (ok) ok = mbar_wait(bar, count & 1, dead, A.flag);
+                ok = __all_sync(0xffffffffu, ok);
                 tc_fence_after();
-                return ok;
             };
-            auto full = [&](uint32_t k) { return wait(bar_full + 8 * (k % kStages), k / kStages); };
-            const uint32_t ring = smem_u32(smem + kOffRing), qs = smem_u32(smem);
-            auto score = [&](int i, uint32_t k) {
+            auto full = [&](uint32_t k) {  // ring tile k has landed
+                if (ok) ok = mbar_wait(bar_full + 8 * (k % kStages), (k / kStages) & 1, dead, A.flag);
+                ok = __all_sync(0xffffffffu, ok);
+            };
+            auto release = [&](uint32_t k) {
+                if (ok) mma_commit(bar_empty + 8 * (k % kStages), leader);
+            };
+            auto score = [&](int i, uint32_t k) {  // S_i = Q_i times the keys in ring tile k
+                if (!ok) return;
                 const uint64_t a = sw128_desc(qs + i * kTileBytes), b = sw128_desc(ring + (k % kStages) * kTileBytes);
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
                     const uint64_t o = (uint64_t)(((t >> 2) * (kTileBytes / 2) + (t & 3) * 32) >> 4);
-                    mma_ss(tmem + 128 * i, a + o, b + o, t > 0);
+                    mma_ss(tmem + 128 * i, a + o, b + o, t > 0, leader);
                 }
-                mma_commit(bar_s + 8 * i);
+                mma_commit(bar_s + 8 * i, leader);
+            };
+            auto weigh = [&](int i, uint32_t k, bool first) {  // O_i += P_i times the values in ring tile k
+                const uint64_t b = sw128_desc(ring + (k % kStages) * kTileBytes);
+                const uint32_t count = np[i]++;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {  // the weights of 96 keys, then of the last 32
+                    wait(bar_p + 16 * hf + 8 * i, count);
+                    if (!ok) return;
+#pragma unroll
+                    for (int t = 6 * hf; t < 6 + 2 * hf; ++t)
+                        mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, b + (uint64_t)(t * 2048 >> 4), (!first || t > 0) ? 1u : 0u, leader);
+                }
+                mma_commit(bar_o + 8 * i, leader);
             };
             while (ok && W.next(x)) {
                 if (x.n == 0) continue;
-                const int tiles = x.rows > 128 ? 2 : 1;
-                for (int i = 0; i < tiles; ++i) {
-                    if (!wait(bar_q + 8 * i, nq[i]++)) break;
-                    if (i == 0 && !full(n)) break;
-                    score(i, n);
-                }
-                if (!ok) break;
-                mma_commit(bar_empty + 8 * (n % kStages));
-                for (int j = 0; j < x.n && ok; ++j) {
-                    const uint32_t v = n + 2 * j + 1, k = v + 1;
-                    for (int i = 0; i < tiles; ++i) {
-                        if (!wait(bar_p + 8 * i, np[i]++)) break;
-                        if (i == 0 && !full(v)) break;
-                        const uint64_t b = sw128_desc(ring + (v % kStages) * kTileBytes);
-#pragma unroll
-                        for (int t = 0; t < 8; ++t)
-                            mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, b + (uint64_t)(t * 2048 >> 4), (j > 0 || t > 0) ? 1u : 0u);
-                        mma_commit(bar_o + 8 * i);
-                        if (i == tiles - 1) mma_commit(bar_empty + 8 * (v % kStages));
-                        if (j + 1 < x.n) {
-                            if (i == 0 && !full(k)) break;
-                            score(i, k);
-                            if (i == tiles - 1) mma_commit(bar_empty + 8 * (k % kStages));
+                if (x.thin()) {
+                    uint32_t at = n;  // next ring tile
+                    for (int i = 0; i < min(2, x.n); ++i) {
+                        wait(bar_q + 8 * i, nq[i]++);
+                        full(at);
+                        score(i, at);
+                        release(at++);
+                    }
+                    for (int j = 0; j < x.n && ok; ++j) {
+                        const int i = j & 1;
+                        full(at);
+                        if (j + 2 < x.n) full(at + 1);
+                        weigh(i, at, j < 2);
+                        release(at++);
+                        if (j + 2 < x.n) {
+                            score(i, at);
+                            release(at++);
+                        }
+                    }
+                } else {
+                    full(n);
+                    for (int i = 0; i < 2; ++i) {
+                        wait(bar_q + 8 * i, nq[i]++);
+                        score(i, n);
+                    }
+                    release(n);
+                    for (int j = 0; j < x.n && ok; ++j) {
+                        const uint32_t v = n + 2 * j + 1, k = v + 1;
+                        full(v);
+                        if (j + 1 < x.n) full(k);
+                        for (int i = 0; i < 2; ++i) {
+                            weigh(i, v, j == 0);
+                            if (i == 1) release(v);
+                            if (j + 1 < x.n) {
+                                score(i, k);
+                                if (i == 1) release(k);
+                            }
                         }
                     }
                 }
@@ -672,25 +807,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
             }
             // every product issued is done before the tensor memory is freed
             uint32_t zero = 0u;
-            mma_commit(bar_end);
+            mma_commit(bar_end, leader);
             mbar_wait(bar_end, 0u, &zero, nullptr);
         }
-    } else if (warp < 8) {
-        // ---- softmax: thread = row `row` of tile i
+    } else {
+        // ---- softmax: a thread a row of engine i
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int i = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128 * i, to = tmem + lanes + 256 + 128 * i;
         uint8_t* qs = smem + i * kTileBytes;
         const uint32_t flip = A.scale < 0.0f ? 0x80008000u : 0u;       // a negative scale turns Q's signs
         const float c = fmaxf(fabsf(A.scale) * 1.44269504f, 1e-30f);  // 0: weights of 1, and masked scores stay -inf
-        uint32_t ns = 0, no = 0;
-        bool ok = true, more;
+        const uint64_t c2 = pair(c, c);
+        uint32_t ns = 0, no = 0, nx[2] = {0, 0};
+        bool ok = true;
+        int4 cut = make_int4(0, -1, 0, 0);
         Part x, y;
         auto load_q = [&](const Part& z) {  // this thread's row of Q, zeros behind the item's rows
-            const int r = i * 128 + row;
+            const int r = z.row0(i) + row;
             uint4 v[16];
             if (r < z.rows) {
-                const int g = z.qt * kRows + r, tok = P.q0[z.b] + g / A.group;
+                const int g = z.qt * kRows + r, tok = P.seqs()[z.b].x + g / A.group;
                 const uint4* src = reinterpret_cast<const uint4*>(
                     A.q + (int64_t)tok * A.q_token + (int64_t)((A.h0 + z.h) * A.group + g % A.group) * A.q_head);
 #pragma unroll
@@ -712,148 +850,195 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
-        auto active = [&](const Part& z) { return z.n > 0 && z.rows > 128 * i; };
-        more = W.next(x);
-        if (more && active(x)) load_q(x);
-        while (more) {
+        float m = -INFINITY, l = 0.0f;  // the row's maximum and sum, over the part so far
+        auto finish = [&]() {            // part x is done: its rows of the output, or of the part's slot
+            const int r = x.row0(i) + row, g = x.qt * kRows + r, n = x.tiles(i);
+            const bool both = x.thin() && x.n > 1;  // a thin part on both engines
+            const bool real = r < x.rows, idle = x.row0(i) + (warp & 3) * 32 >= x.rows;
+            if (n > 0) wait(bar_o + 8 * i, no - 1);
+            if (both && i == 1) {  // O_1 stays in tensor memory until engine 0 has read it
+                s_ml[row] = m;
+                s_ml[128 + row] = l;
+                tc_fence_before();
+                mbar_arrive(bar_x);
+                ++nx[1];
+            } else if (x.row0(i) < x.rows && (i == 0 || !x.thin())) {
+                float f0 = 1.0f, f1 = 0.0f;
+                if (both) {
+                    wait(bar_x, nx[0]++);
+                    const float m1 = s_ml[row], l1 = s_ml[128 + row], mn = fmaxf(m, m1);
+                    f0 = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
+                    f1 = m1 == -INFINITY ? 0.0f : ex2((m1 - mn) * c);
+                    l = l * f0 + l1 * f1;
+                    m = mn;
+                }
+                const bool whole = x.begins && x.ends;
+                const int64_t slot = 2 * (int64_t)blockIdx.x + (x.begins ? 1 : 0);
+                const int64_t at = (int64_t)P.seqs()[x.b].x + (real ? g / A.group : 0);
+                const int qh = (A.h0 + x.h) * A.group + g % A.group;
+                if (whole) {
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    f0 *= inv;
+                    f1 *= inv;
+                }
+                if (!idle) {
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[32], o1[32];
+                        __syncwarp();
+                        if (n > 0) {
+                            tmem_ld32(to + 32 * k, o);
+                            if (both) tmem_ld32(to + 128 + 32 * k, o1);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int t = 0; t < 32; ++t) {
+                                const float e = __uint_as_float(o[t]) * f0;
+                                o[t] = __float_as_uint(both ? fmaf(__uint_as_float(o1[t]), f1, e) : e);
+                            }
+                        } else {  // the row sees no key
+#pragma unroll
+                            for (int t = 0; t < 32; ++t) o[t] = 0u;
+                        }
+                        if (!ok || !real) {
+                        } else if (whole) {
+                            uint4* dst = reinterpret_cast<uint4*>(A.out + at * A.out_token + (int64_t)qh * A.out_head) + 4 * k;
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = pack_bf16x2(__uint_as_float(o[8 * t + 2 * e]), __uint_as_float(o[8 * t + 2 * e + 1]));
+                                dst[t] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+                            uint4* dst = reinterpret_cast<uint4*>(A.part_o) + (slot * 32 + 8 * k) * A.slot_rows + r;
+#pragma unroll
+                            for (int t = 0; t < 8; ++t)
+                                dst[t * A.slot_rows] = make_uint4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
+                        }
+                    }
+                    if (ok && real) {
+                        if (whole) {
+                            if (A.lse)
+                                A.lse[at * A.p.kv_heads * A.group + qh] =
+                                    l == 0.0f ? -INFINITY : fmaf(m, c * 0.69314718f, logf(l));
+                        } else {
+                            A.part_ml[(slot * 2) * A.slot_rows + r] = m == -INFINITY ? -INFINITY : m * c;
+                            A.part_ml[(slot * 2 + 1) * A.slot_rows + r] = l;
+                        }
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();  // O is read before the next part's first product is allowed in
+                if (both) mbar_arrive(bar_x + 8);
+            }
+            if (x.begins && !x.ends) cut = make_int4(x.b, x.h, x.qt, (int)(((x.last + 1) * shares - 1) / total));
+        };
+        // one pass more than parts: Q of the next part is loaded, and its first
+        // products can start, before this one's output is written
+        for (bool have = false;; have = true) {
             const bool has = W.next(y);
-            const int r = i * 128 + row, g = x.qt * kRows + r;
+            if (has && y.active(i)) load_q(y);  // the scores that read the last Q are done
+            if (have) finish();
+            if (!has) break;
+            x = y;
+            const int r = x.row0(i) + row, n = x.tiles(i), step = x.thin() ? 2 : 1;
             const Seq s = P.seq(x.b);
-            const bool real = r < x.rows;
-            const int tok = real ? g / A.group : 0;
+            const bool real = r < x.rows, idle = x.row0(i) + (warp & 3) * 32 >= x.rows;  // idle: no row of this warp is one
+            const int tok = real ? (x.qt * kRows + r) / A.group : 0;
             int klo, khi;  // keys that this row sees
             visible(s, window, tok, tok, klo, khi);
             if (!real) klo = khi = 0;
             // and those that every row of this tile sees: no mask for key tiles inside them
             int alo, ahi;
             {
-                const int last = min(x.qt * kRows + 128 * i + 127, x.qt * kRows + x.rows - 1) / A.group;
-                const int first = (x.qt * kRows + 128 * i) / A.group;
-                ahi = min(s.keys, s.base + first + 1);
-                alo = window > 0 ? max(0, s.base + last - window + 1) : 0;
+                const int r0 = x.qt * kRows + x.row0(i), r1 = min(r0 + 127, x.qt * kRows + x.rows - 1);
+                ahi = min(s.keys, s.base + r0 / A.group + 1);
+                alo = window > 0 ? max(0, s.base + r1 / A.group - window + 1) : 0;
             }
-            float m = -INFINITY, l = 0.0f;
-            if (active(x)) {
-                for (int j = 0; j < x.n; ++j) {
-                    const int k0 = (x.t0 + j) * kTile;
-                    wait(bar_s + 8 * i, ns++);
-                    uint32_t v[128];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, v + 32 * k);
-                    tmem_wait_ld();
-                    if (k0 < alo || k0 + kTile > ahi) {
-                        const int lo = klo - k0, hi = khi - k0;
-#pragma unroll
-                        for (int k = 0; k < 128; ++k)
-                            if (k < lo || k >= hi) v[k] = 0xff800000u;
-                    }
-                    float top[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(v[k]);
-#pragma unroll
-                    for (int k = 4; k < 128; k += 4)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) top[t] = fmaxf(top[t], __uint_as_float(v[k + t]));
-                    const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                    if (j == 0) {
-                        m = mt;
-                    } else if (__any_sync(0xffffffffu, (mt - m) * c > 8.0f)) {
-                        const float mn = fmaxf(m, mt), f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
-                        m = mn;
-                        l *= f;
-                        wait(bar_o + 8 * i, no - 1);
-#pragma unroll 1
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t o[32];
-                            tmem_ld32(to + 32 * k, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
-                            tmem_st32(to + 32 * k, o);
-                        }
-                    }
-                    const float mc = m == -INFINITY ? 0.0f : m * c;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int k = 0; k < 128; ++k) {
-                        const float e = ex2(fmaf(__uint_as_float(v[k]), c, -mc));
-                        sum[k & 3] += e;
-                        v[k] = __float_as_uint(e);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            pk[k] = pack_bf16x2(__uint_as_float(v[64 * hf + 2 * k]), __uint_as_float(v[64 * hf + 2 * k + 1]));
-                        tmem_st32(ts + 32 * hf, pk);
-                    }
-                    tmem_wait_st();
+            m = -INFINITY;
+            l = 0.0f;
+            for (int j = 0; j < n; ++j) {
+                const int k0 = (x.t0 + (x.thin() ? i : 0) + j * step) * kTile;
+                wait(bar_s + 8 * i, ns++);
+                if (j == 0 && i == 1 && nx[1] > 0) wait(bar_x + 8, nx[1] - 1);  // engine 0 has read the last thin part's O_1
+                if (idle) {  // its lanes of P are whatever they are: rows do not mix
                     tc_fence_before();
                     mbar_arrive(bar_p + 8 * i);
+                    mbar_arrive(bar_p + 16 + 8 * i);
                     ++no;
+                    continue;
                 }
-            }
-            if (has && active(y)) load_q(y);  // the scores that read Q are done
-            if (x.rows > 128 * i) {
-                if (x.n > 0) wait(bar_o + 8 * i, no - 1);
-                const bool whole = x.begins && x.ends;
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (x.begins ? 1 : 0);
-                const int64_t at = (int64_t)s.q0 + tok;
-                const int qh = (A.h0 + x.h) * A.group + g % A.group;
-                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+                if (k0 < alo || k0 + kTile > ahi) {
+                    // keys that the row does not see: -infinity, written back, so that the
+                    // few such tiles share the code below (a second copy of it cost every
+                    // small call 10 us of instruction fetches)
+                    const int lo = klo - k0, hi = khi - k0;
 #pragma unroll 1
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t o[32];
-                    __syncwarp();
-                    if (x.n > 0) {
-                        tmem_ld32(to + 32 * k, o);
+                    for (int k = 0; k < 128; k += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(ts + k, o);
                         tmem_wait_ld();
-                    } else {  // the row sees no key
 #pragma unroll
-                        for (int t = 0; t < 32; ++t) o[t] = 0u;
+                        for (int t = 0; t < 16; ++t)
+                            if (k + t < lo || k + t >= hi) o[t] = 0xff800000u;
+                        tmem_st16(ts + k, o);
                     }
-                    if (!ok || !real) {
-                    } else if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(A.out + at * A.out_token + (int64_t)qh * A.out_head) + 4 * k;
+                    tmem_wait_st();
+                }
+                uint32_t v[128];
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            uint32_t w[4];
+                for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, v + 32 * k);
+                tmem_wait_ld();
+                float top[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = pack_bf16x2(__uint_as_float(o[8 * t + 2 * e]) * inv, __uint_as_float(o[8 * t + 2 * e + 1]) * inv);
-                            dst[t] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(A.part_o) + (slot * 32 + 8 * k) * A.slot_rows + r;
+                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(v[k]);
 #pragma unroll
-                        for (int t = 0; t < 8; ++t)
-                            dst[t * A.slot_rows] = make_uint4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
+                for (int k = 4; k < 124; k += 8)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        top[t] = fmaxf(top[t], fmaxf(__uint_as_float(v[k + t]), __uint_as_float(v[k + 4 + t])));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) top[t] = fmaxf(top[t], __uint_as_float(v[124 + t]));
+                const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                if (j == 0) {
+                    m = mt;
+                } else if (__any_sync(0xffffffffu, (mt - m) * c > 8.0f)) {
+                    const float mn = fmaxf(m, mt), f = mn == -INFINITY ? 1.0f : ex2((m - mn) * c);
+                    m = mn;
+                    l *= f;
+                    wait(bar_o + 8 * i, no - 1);
+#pragma unroll 1
+                    for (int k = 0; k < 128; k += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(to + k, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int t = 0; t < 16; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
+                        tmem_st16(to + k, o);
                     }
                 }
-                if (ok && real) {
-                    if (whole) {
-                        if (A.lse)
-                            A.lse[at * A.p.kv_heads * A.group + qh] =
-                                l == 0.0f ? -INFINITY : fmaf(m, c * 0.69314718f, logf(l));
-                    } else {
-                        A.part_ml[(slot * 2) * A.slot_rows + r] = m == -INFINITY ? -INFINITY : m * c;
-                        A.part_ml[(slot * 2 + 1) * A.slot_rows + r] = l;
+                const float mc = m == -INFINITY ? 0.0f : -m * c;
+                const uint64_t mc2 = pair(mc, mc);
+                uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t w[16];
+                    weights(v + 32 * k, c2, mc2, w, sum);
+                    tmem_st16(ts + 16 * k, w);
+                    if (k >= 2) {  // the first 96 keys' weights, then the last 32
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(bar_p + 16 * (k - 2) + 8 * i);
                     }
                 }
-                tc_fence_before();  // O is read before the next part's first product is allowed in
+                ++no;
+                float a, b;
+                unpair(add2(sum[0], sum[1]), a, b);
+                l += a + b;
             }
-            if (tid == 0 && x.begins && !x.ends) {
-                const long long last = x.at + x.units - 1;
-                A.part_item[blockIdx.x] = make_int4(x.b, x.h, x.qt, (int)(((last + 1) * shares - 1) / total));
-            }
-            if (tid == 0 && !has && (!x.begins || x.ends)) A.part_item[blockIdx.x] = make_int4(0, -1, 0, 0);
-            x = y;
-            more = has;
         }
-        __syncwarp();
-        if (tid == 0 && !works) A.part_item[blockIdx.x] = make_int4(0, -1, 0, 0);
+        if (tid == 0) A.part_item[blockIdx.x] = cut;
     }
     tc_fence_before();
     __syncthreads();
