@@ -76,7 +76,7 @@ extern "C" int ecco_rope(const void* x, int64_t x_token, int64_t x_head, void* y
                          int rotary, const int32_t* positions, int flags, void* stream)
 {
     if (dtype != ECCO_BF16 && dtype != ECCO_F16 && dtype != ECCO_F32) return ECCO_ERR_ARG;
-    if (tokens < 0 || tokens > ((int64_t)1 << 31) || heads < 1 || heads > 65535) return ECCO_ERR_ARG;
+    if (tokens < 0 || tokens > 0x7fffffff || heads < 1 || heads > 65535) return ECCO_ERR_ARG;
     if (dim < 8 || dim > 1024 || dim % 8 || rotary < 16 || rotary > dim || rotary % 16) return ECCO_ERR_ARG;
     if (n_positions < 1 || n_positions > ((int64_t)1 << 30)) return ECCO_ERR_ARG;
     if (flags & ~(ECCO_ROPE_INTERLEAVED | ECCO_ROPE_INVERSE)) return ECCO_ERR_ARG;

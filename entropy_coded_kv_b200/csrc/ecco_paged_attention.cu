@@ -99,6 +99,70 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c)
     return (uint32_t)((c >> 3) * (kTileBytes / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// ------------------------------------------------------------ barriers, copies, launches
+constexpr uint32_t kSpinLimit = 1u << 20;
+__device__ unsigned int g_timeouts = 0;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// One untiled copy to shared memory, counted on `bar` (16-byte aligned, a
+// multiple of 16 bytes).
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Waits for the phase of the given parity: at most kSpinLimit polls of up to a
+// microsecond.  A wait that gives up counts itself, raises the host-visible
+// flag and marks the CTA dead, so that its other waits end too.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead, int* flag)
+{
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (*dead) return false;
+    }
+    *dead = 1u;
+    atomicAdd(&g_timeouts, 1u);
+    if (flag) {
+        *reinterpret_cast<volatile int*>(flag) = 1;
+        __threadfence_system();
+    }
+    return false;
+}
+
+// The kernels of a call follow one another with programmatic launches: the
+// next one's CTAs may start (and plan, and load their queries) once every CTA
+// has come this far and left its SM; they wait with after_previous() before
+// they touch what the previous kernel writes.  Every CTA of a kernel waits, so
+// that its end means the previous one's.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------ decode into tiles
 constexpr int kDecThreads = 896;
 constexpr size_t kDecLut = sizeof(((DevTables*)0)->lut), kDecCt = sizeof(((DevTables*)0)->Ct);
@@ -112,22 +176,17 @@ struct StageArgs {
     const uint8_t* pages[2];
     uint8_t* scratch;  // [2][heads of the round][tiles][kTileBytes]
     int h0, hn;
+    bool wide;  // pools 32-byte aligned: 32-byte loads
+    int* flag;
 };
 
-// Stores values 16 j .. 16 j + 15 of a row: its 32-byte piece, the two halves
-// swapped in odd rows.
-__device__ __forceinline__ void store_piece(uint8_t* row, uint32_t x, int j, const uint32_t a[4], const uint32_t b[4])
-{
-    uint8_t* d = row + (j >> 2) * (kTileBytes / 2) + (((j & 3) ^ (x >> 1)) << 5);
-    if (x & 1u)
-        stg256(d, b, a);
-    else
-        stg256(d, a, b);
-}
-
+// The first half of the CTAs decodes the keys, the second the values, each an
+// equal run of rows of the round's tiles, one row a thread; a CTA's tables come
+// by bulk copies while it works out where its rows are.
 __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __grid_constant__ StageArgs A)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_bar;
     uint8_t* smem = aligned_smem(smem_raw);
     uint8_t* s_lut = smem;
     float* s_Ct = reinterpret_cast<float*>(smem + kDecLut);
@@ -136,7 +195,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     int* s_first = s_cu + ECCO_MAX_BATCH + 1;                    // [batch] its first tile
     const int tid = threadIdx.x;
     uint32_t* ws = s_w + tid;
+    const int half = gridDim.x / 2, kv = blockIdx.x >= half;
+    const DevTables* tb = A.tb[kv];
+    launch_dependents();
 
+    const uint32_t bar = smem_u32(&s_bar);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        mbar_expect(bar, (uint32_t)(kDecLut + kDecCt));
+        bulk_copy(smem_u32(s_lut), &tb->lut[0][0], (uint32_t)kDecLut, bar);
+        bulk_copy(smem_u32(s_Ct), &tb->Ct[0][0], (uint32_t)kDecCt, bar);
+    }
     for (int b = tid; b < A.p.batch; b += kDecThreads) {
         int first, count;
         seq_tiles(seq_of(A.p, A.w, b), A.w.window, first, count);
@@ -147,77 +217,98 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     if (tid < 32) warp_prefix(s_cu, A.p.batch, tid);
     __syncthreads();
     const int tiles = s_cu[A.p.batch];
-    const int64_t each = (int64_t)tiles * A.hn * kTile, total = 2 * each;
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t begin = (int64_t)blockIdx.x * share, end = min(total, begin + share);
+    const int64_t total = (int64_t)tiles * A.hn * kTile;
+    const int64_t share = ((total + half - 1) / half + 1) & ~(int64_t)1;  // even, so that lane pairs stay together
+    const int64_t lo = (int64_t)(blockIdx.x - kv * half) * share, hi = min(total, lo + share);
+    const uint8_t* pool = A.pages[kv];
+    uint8_t* out = A.scratch + (int64_t)kv * A.hn * tiles * kTileBytes;
 
-    for (int kv = 0; kv < 2; ++kv) {
-        const int64_t lo = max(begin, kv * each) - kv * each, hi = min(end, (kv + 1) * each) - kv * each;
-        if (lo >= hi) continue;
-        const DevTables* tb = A.tb[kv];
-        const uint8_t* pool = A.pages[kv];
-        uint8_t* out = A.scratch + (int64_t)kv * A.hn * tiles * kTileBytes;
-        __syncthreads();  // the keys' tables are no longer read
-        stage_tables<kDecThreads>(tb, s_lut, s_Ct, tid);
-        const float S_t = tb->S_t;
-        __syncthreads();
-
-        // the source block of row `i` of the round, or null: past the keys, or in no page
-        auto locate = [&](int64_t i) -> const uint8_t* {
-            const int lin = (int)(i >> 7), h = lin / tiles, tile = lin - h * tiles;
-            const int b = find_seq(s_cu, A.p.batch, tile);
-            const int t = (s_first[b] + tile - s_cu[b]) * kTile + (int)(i & (kTile - 1));
-            if (t >= paged_kv_len(A.p, b, A.w.max_kv)) return nullptr;
-            const int64_t blk = paged_block(A.p, b, A.h0 + h, t);
-            return blk < 0 ? nullptr : pool + blk * ECCO_BLOCK_BYTES;
-        };
-        const int part = (int)(hi - lo);
-        const int rounds = (part + kDecThreads - 1) / kDecThreads, per_round = (part + rounds - 1) / rounds;
-        const int64_t stop = (tid < per_round) ? hi : 0;
-        int64_t i = lo + tid;
-        const uint8_t* src = i < stop ? locate(i) : nullptr;
-        for (; i < stop; i += per_round) {
-            uint8_t* row = out + (i >> 7) * kTileBytes + (i & (kTile - 1)) * 128;
-            const uint32_t x = (uint32_t)(i & 7);
-            uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0, q2 = q0, q3 = q0;
-            if (src) {
+    // the source block of row `i` of the round, or null: past the keys, or in no page
+    auto locate = [&](int64_t i) -> const uint8_t* {
+        const int lin = (int)(i >> 7), h = lin / tiles, tile = lin - h * tiles;
+        const int b = find_seq(s_cu, A.p.batch, tile);
+        const int t = (s_first[b] + tile - s_cu[b]) * kTile + (int)(i & (kTile - 1));
+        if (t >= paged_kv_len(A.p, b, A.w.max_kv)) return nullptr;
+        const int64_t blk = paged_block(A.p, b, A.h0 + h, t);
+        return blk < 0 ? nullptr : pool + blk * ECCO_BLOCK_BYTES;
+    };
+    const int part = (int)max(hi - lo, (int64_t)0);
+    const int rounds = max(1, (part + kDecThreads - 1) / kDecThreads), per_round = ((part + rounds - 1) / rounds + 1) & ~1;
+    const int64_t stop = (tid < per_round) ? hi : 0;
+    int64_t i = lo + tid;
+    const uint8_t* src = i < stop ? locate(i) : nullptr;
+    uint32_t dead = 0u;
+    if (!mbar_wait(bar, 0u, &dead, A.flag)) return;  // no tables: nothing is decoded, and the flag says so
+    const float S_t = tb->S_t;
+    for (; i < stop; i += per_round) {
+        const int here = min((int)(hi - (i - (tid & 31))), per_round - (tid & ~31));  // rows of this warp in the round: even
+        const unsigned pm = here >= 32 ? 0xffffffffu : (1u << here) - 1u;
+        uint8_t* even = out + (i >> 7) * kTileBytes + (i & (kTile - 2)) * 128;  // the pair's first row (an even one)
+        const uint32_t x = (uint32_t)(i & 7);
+        uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0, q2 = q0, q3 = q0;
+        if (src) {
+            if (A.wide) {
+                ldg_nc_v8(src, q0, q1);
+                ldg_nc_v8(src + 32, q2, q3);
+            } else {
                 q0 = ldg_nc_v4(src);
                 q1 = ldg_nc_v4(src + 16);
                 q2 = ldg_nc_v4(src + 32);
                 q3 = ldg_nc_v4(src + 48);
             }
-            if (i + per_round < stop) {  // this thread's next block: on its way to L2 while this one decodes
-                src = locate(i + per_round);
-                if (src) asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
-            }
-            const uint32_t code = q0.x & 0xffu;
-            if (scale_code_is_null(code)) {
-                const uint32_t z[4] = {0u, 0u, 0u, 0u};
+        }
+        if (i + per_round < stop) {  // this thread's next block: on its way to L2 while this one decodes
+            src = locate(i + per_round);
+            if (src) asm volatile("prefetch.global.L2 [%0];" ::"l"(src));
+        }
+        const uint32_t code = q0.x & 0xffu;
+        const bool null = scale_code_is_null(code);
+        stage_words(ws, kDecThreads, q0, q1, q2, q3);
+        const int p = (int)((q0.x >> 8) & 63u);
+        const uint32_t lkey = lut_key(s_lut, (q0.x >> 8) & 255u);
+        const float s = __fmul_rn(S_t, e4m3_to_f32(code));
+        ValuePlanes vp = make_planes(s, s_Ct, p);
+        if (null) {  // 128 times +0, whatever the stream says
 #pragma unroll
-                for (int j = 0; j < kG / 16; ++j) store_piece(row, x, j, z, z);
-                continue;
-            }
-            stage_words(ws, kDecThreads, q0, q1, q2, q3);
-            const int p = (int)((q0.x >> 8) & 63u);
-            const uint32_t lkey = lut_key(s_lut, (q0.x >> 8) & 255u);
-            const float s = __fmul_rn(S_t, e4m3_to_f32(code));
-            const ValuePlanes vp = make_planes(s, s_Ct, p);
-            Stream st{q0.x, q0.y, kHdrBits, 2, kPayloadBits};
+            for (int k = 0; k < 4; ++k) vp.lo[k] = vp.hi[k] = 0u;
+        }
+        Stream st{q0.x, q0.y, kHdrBits, 2, kPayloadBits};
+        // Lanes 2k and 2k + 1 store 64 contiguous bytes of one row an instruction
+        // (ecco_decode.cu measured the pairing): each sends its partner the 16
+        // values that belong to the partner's store.  A 32-byte piece stays a
+        // piece under the swizzle, its halves swapped in odd rows.
+        const bool odd = tid & 1;
 #pragma unroll 1
-            for (int j = 0; j < kG / 16; ++j) {
-                uint32_t wa[4], wb[4];
-                chunk_values(st, lkey, ws, kDecThreads, vp, wa);
-                chunk_values(st, lkey, ws, kDecThreads, vp, wb);
-                store_piece(row, x, j, wa, wb);
+        for (int c = 0; c < kG / 16; c += 2) {
+            uint32_t a0[4], b0[4], a1[4], b1[4], ra[4], rb[4];
+            chunk_values(st, lkey, ws, kDecThreads, vp, a0);
+            chunk_values(st, lkey, ws, kDecThreads, vp, b0);
+            chunk_values(st, lkey, ws, kDecThreads, vp, a1);
+            chunk_values(st, lkey, ws, kDecThreads, vp, b1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // the even lane sends piece c + 1, the odd lane piece c
+                ra[k] = __shfl_xor_sync(pm, odd ? a0[k] : a1[k], 1);
+                rb[k] = __shfl_xor_sync(pm, odd ? b0[k] : b1[k], 1);
             }
-            if (st.room >= 0) {  // unclipped: outlier records follow the codewords
-                const int n = min(kMaxRec, st.room / kRecBits), at0 = kBlockBits - st.room;
-                for (int k = 0; k < n; ++k) {
-                    const uint32_t rec = read_record(ws, kDecThreads, at0 + k * kRecBits), e = rec & 127u;
-                    const float o = q_over_127((int)(int8_t)(uint8_t)(rec >> 7));
-                    *reinterpret_cast<uint16_t*>(row + (e >> 6) * (kTileBytes / 2) + ((((e >> 3) & 7u) ^ x) << 4) +
-                                                 (e & 7u) * 2) = (uint16_t)f32_to_bf16_bits(__fmul_rn(s, o));
-                }
+            const int j = c + odd;
+            uint8_t* d = even + (j >> 2) * (kTileBytes / 2) + (((j & 3) ^ (x >> 1)) << 5);
+            if (odd) {
+                stg256(d, ra, rb);
+                stg256(d + 128, b1, a1);
+            } else {
+                stg256(d, a0, b0);
+                stg256(d + 128, rb, ra);
+            }
+        }
+        __syncwarp(pm);  // the partner's part of this row is stored before the records change it
+        if (!null && st.room >= 0) {  // unclipped: outlier records follow the codewords
+            uint8_t* row = even + (odd ? 128 : 0);
+            const int n = min(kMaxRec, st.room / kRecBits), at0 = kBlockBits - st.room;
+            for (int k = 0; k < n; ++k) {
+                const uint32_t rec = read_record(ws, kDecThreads, at0 + k * kRecBits), e = rec & 127u;
+                const float o = q_over_127((int)(int8_t)(uint8_t)(rec >> 7));
+                *reinterpret_cast<uint16_t*>(row + (e >> 6) * (kTileBytes / 2) + ((((e >> 3) & 7u) ^ x) << 4) +
+                                             (e & 7u) * 2) = (uint16_t)f32_to_bf16_bits(__fmul_rn(s, o));
             }
         }
     }
@@ -275,14 +366,11 @@ constexpr size_t kOffBars = kOffRing + (size_t)kStages * kTileBytes;
 constexpr size_t kOffUnits = kOffBars + kBars * 8 + 24 + 1024;
 constexpr size_t kOffSeq = (kOffUnits + (ECCO_MAX_BATCH + 1) * 8 + 15) / 16 * 16;
 constexpr size_t kAttnSmem = 1024 + kOffSeq + sizeof(int) * (5 * ECCO_MAX_BATCH + 1);
-constexpr uint32_t kSpinLimit = 1u << 20;
 // Registers a thread: 384 threads start with 168 (65,536 / 384, in eights);
 // the softmax warps take 216, the other warpgroup gives up 96 of its 168:
 // 256 * 216 + 128 * 72 = 64,512 = 384 * 168.
 constexpr int kSoftRegs = 216, kIssueRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kIssueRegs <= kAttnThreads * 168, "more registers than the block was launched with");
-
-__device__ unsigned int g_timeouts = 0;
 
 // D fp32, A and B bf16, N = 128, M = 128; kIdescPV: B N-major (bit 16).
 constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
@@ -295,44 +383,6 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr)
 {
     return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)((kTileBytes / 2) >> 4) << 16) | ((uint64_t)(1024u >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
-}
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Waits for the phase of the given parity: at most kSpinLimit polls of up to a
-// microsecond.  A wait that gives up counts itself, raises the host-visible
-// flag and marks the CTA dead, so that its other waits end too.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead, int* flag)
-{
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (done) return true;
-        if (*dead) return false;
-    }
-    *dead = 1u;
-    atomicAdd(&g_timeouts, 1u);
-    if (flag) {
-        *reinterpret_cast<volatile int*>(flag) = 1;
-        __threadfence_system();
-    }
-    return false;
 }
 
 // The issuing warp runs as a whole (`leader` is true in one lane), so that the
@@ -561,6 +611,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
     P.batch = A.p.batch;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int window = A.w.window;
+    launch_dependents();
 
     // ---- plan
     if (tid == 0) {
@@ -689,6 +740,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
         if (warp == 9 && lane == 0) {
             // ---- copies
+            after_previous();  // the tiles are decoded
             Part x;
             uint32_t n = 0;
             bool ok = true;
@@ -697,13 +749,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                 auto copy = [&](int j, bool v) {
                     const uint32_t st = n % kStages, use = n / kStages;
                     if (!ok || (use > 0 && !(ok = mbar_wait(bar_empty + 8 * st, (use - 1) & 1, dead, A.flag)))) return;
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar_full + 8 * st), "r"(kTileBytes)
-                                 : "memory");
-                    asm volatile(
-                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                            smem_u32(smem + kOffRing) + st * kTileBytes),
-                        "l"(src + (int64_t)j * kTileBytes + (v ? v_offset : 0)), "r"(kTileBytes), "r"(bar_full + 8 * st)
-                        : "memory");
+                    mbar_expect(bar_full + 8 * st, kTileBytes);
+                    bulk_copy(smem_u32(smem + kOffRing) + st * kTileBytes, src + (int64_t)j * kTileBytes + (v ? v_offset : 0),
+                              kTileBytes, bar_full + 8 * st);
                     ++n;
                 };
                 const int ahead = x.thin() ? 2 : 1;
@@ -1047,32 +1095,40 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
 }
 
 // Joins the parts of the items that were cut: block (c, piece) the item that
-// CTA c began and left unfinished.  A thread joins 4 values of a row.
+// CTA c began and left unfinished.  A thread joins 4 values of a row; a warp
+// has 8 rows by 4 such pieces, which is 128 bytes of every part's columns and
+// a whole 32-byte sector of every output row.
 constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnArgs A)
 {
+    after_previous();
     const int4 it = A.part_item[blockIdx.x];
     if (it.y < 0) return;
     const Seq s = seq_of(A.p, A.w, it.x);
     const int rows = min(kRows, s.q * A.group - it.z * kRows);
-    const int at = blockIdx.y * kJoinThreads + threadIdx.x;
-    if (at >= rows * 32) return;
-    const int r = at % rows, c4 = at / rows;
+    const int at = blockIdx.y * kJoinThreads + threadIdx.x;  // (8 rows, 8 groups of 4 pieces, 4 pieces, row)
+    const int r = (at >> 8) * 8 + (at & 7), c4 = (at >> 3) & 31;
+    if (r >= rows) return;
     const int c0 = blockIdx.x, c1 = it.w;
-    auto slot = [&](int c) -> int64_t { return 2 * (int64_t)c + (c == c0 ? 1 : 0); };
-    float m = -INFINITY, l = 0.0f;
-    for (int c = c0; c <= c1; ++c) m = fmaxf(m, A.part_ml[slot(c) * 2 * A.slot_rows + r]);
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = c0; c <= c1; ++c) {
-        const float mc = A.part_ml[slot(c) * 2 * A.slot_rows + r];
-        const float f = mc == -INFINITY ? 0.0f : exp2f(mc - m);
-        l += f * A.part_ml[(slot(c) * 2 + 1) * A.slot_rows + r];
-        const float4 v = reinterpret_cast<const float4*>(A.part_o)[(slot(c) * 32 + c4) * A.slot_rows + r];
-        o.x += f * v.x;
-        o.y += f * v.y;
-        o.z += f * v.z;
-        o.w += f * v.w;
+    const int64_t step = 2 * (int64_t)A.slot_rows;  // from slot to slot of part_ml; part_o has 16 times as many float4
+    const float* ml = A.part_ml + (2 * (int64_t)c0 + 1) * step + r;  // slot 2 c0 + 1, then 2 c of the others
+    const float4* po = reinterpret_cast<const float4*>(A.part_o) + (2 * (int64_t)c0 + 1) * 16 * step + (int64_t)c4 * A.slot_rows + r;
+    float m = ml[0], l = ml[A.slot_rows];
+    float4 o = *po;
+    ml += step;
+    po += 16 * step;
+#pragma unroll 4
+    for (int c = c0 + 1; c <= c1; ++c, ml += 2 * step, po += 32 * step) {
+        const float mc = ml[0], lc = ml[A.slot_rows];
+        const float4 v = *po;
+        const float mn = fmaxf(m, mc), f = m == -INFINITY ? 0.0f : exp2f(m - mn), g = mc == -INFINITY ? 0.0f : exp2f(mc - mn);
+        m = mn;
+        l = l * f + lc * g;
+        o.x = o.x * f + v.x * g;
+        o.y = o.y * f + v.y * g;
+        o.z = o.z * f + v.z * g;
+        o.w = o.w * f + v.w * g;
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int g = it.z * kRows + r, qh = (A.h0 + it.y) * A.group + g % A.group;
@@ -1120,6 +1176,23 @@ size_t paged_attention_bytes(int batch, int kv_heads, int group, int max_q, int 
 
 cudaError_t paged_timeouts(unsigned int* n) { return cudaMemcpyFromSymbol(n, g_timeouts, sizeof(*n)); }
 
+// Launches a kernel whose CTAs may start before the previous kernel has ended
+// (it waits with after_previous).
+static cudaError_t launch_after(void (*kernel)(AttnArgs), dim3 grid, int threads, size_t smem, cudaStream_t s, const AttnArgs& a)
+{
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, a);
+}
+
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* workspace, cudaStream_t s)
 {
     static std::atomic<uint64_t> configured[2]{};
@@ -1132,18 +1205,19 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* workspace, cuda
     const int hn = round_heads(a.p.batch, a.p.kv_heads, a.max_kv);
     const int ctas = std::min(device_sm_count(), kMaxCtas);
     const Bounds w{a.tokens, a.max_q, a.max_kv, a.window};
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.pages[0]) | reinterpret_cast<uintptr_t>(a.pages[1])) & 31u) == 0;
     for (int h0 = 0; h0 < a.p.kv_heads; h0 += hn) {
         const int n = std::min(hn, a.p.kv_heads - h0);
-        const StageArgs st{a.p, w, {a.tb[0], a.tb[1]}, {a.pages[0], a.pages[1]}, scratch, h0, n};
-        paged_decode_kernel<<<device_sm_count(), kDecThreads, kDecSmem, s>>>(st);
+        const StageArgs st{a.p, w, {a.tb[0], a.tb[1]}, {a.pages[0], a.pages[1]}, scratch, h0, n, wide, timeout_flag()};
+        // (the first kernel of a round waits for all before it: the workspace is free)
+        paged_decode_kernel<<<std::max(2, device_sm_count() & ~1), kDecThreads, kDecSmem, s>>>(st);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         const AttnArgs at{a.p, w, scratch, a.q, a.out, a.lse, a.q_token, a.q_head, a.out_token, a.out_head, a.group, h0, n,
                           a.scale, reinterpret_cast<float*>(ws + L.o), reinterpret_cast<float*>(ws + L.ml),
                           reinterpret_cast<int4*>(ws), L.slot_rows, timeout_flag()};
-        paged_attention_kernel<<<ctas, kAttnThreads, kAttnSmem, s>>>(at);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        paged_join_kernel<<<dim3(ctas, (L.slot_rows * 32 + kJoinThreads - 1) / kJoinThreads), kJoinThreads, 0, s>>>(at);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_after(paged_attention_kernel, dim3(ctas), kAttnThreads, kAttnSmem, s, at)) != cudaSuccess) return e;
+        const dim3 join(ctas, ((L.slot_rows + 7) / 8 * 256 + kJoinThreads - 1) / kJoinThreads);
+        if ((e = launch_after(paged_join_kernel, join, kJoinThreads, 0, s, at)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

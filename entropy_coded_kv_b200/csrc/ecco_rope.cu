@@ -26,6 +26,7 @@ __global__ void rope_table_kernel(const __grid_constant__ Freqs F, int n_freq, d
 }
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 4;  // heads whose loads a thread has in flight (y may be x: the compiler cannot move a load over a store)
 
 template <typename T>
 struct Vec8 {  // 8 values: 16 bytes of a 16-bit type, 32 of fp32
@@ -48,44 +49,74 @@ __device__ __forceinline__ void store8(T* p, const Vec8<T>& v)
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = v.w[i];
 }
 
-// A thread turns one unit of a head: 8 pairs (values 8u.. and their partners
-// rotary / 2 further on, or 16 values in a row), or copies 8 values behind
-// the turned part.
+// A thread has one unit of a token's heads: pieces u and u + rotary / 16 of 8
+// values, turned together -- halves: value k of the one with value k of the
+// other; interleaved: each has its own pairs -- or two pieces behind the turned
+// part, copied.  Neighbouring threads have neighbouring pieces, whatever they
+// do with them.  A thread does so for every head h0, h0 + groups, .. of the
+// token, so cos and sin are loaded once for them and the heads' loads overlap.
+// `per` = units * groups threads a token, 32-bit indices inside it.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs A, int units, int64_t total)
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs A, int units, int groups,
+                                                        int tokens_per_block)
 {
-    const int pairs8 = A.rotary / 16;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t th = i / units, t = th / A.heads;
-        const int u = (int)(i - th * units), h = (int)(th - t * A.heads);
-        const T* x = static_cast<const T*>(A.x) + t * A.x_token + h * A.x_head;
-        T* y = static_cast<T*>(A.y) + t * A.y_token + h * A.y_head;
-        if (u >= pairs8) {
-            const int at = A.rotary + 8 * (u - pairs8);
-            store8(y + at, load8(x + at));
-            continue;
-        }
-        const int ia = A.interleaved ? 16 * u : 8 * u, ib = A.interleaved ? ia + 8 : ia + A.rotary / 2;
-        Vec8<T> a = load8(x + ia), b = load8(x + ib);
-        const int64_t pos = min(max((int64_t)A.positions[t], (int64_t)0), A.n_positions - 1);
-        const float4* cs = reinterpret_cast<const float4*>(A.table + (pos * (A.rotary / 2) + 8 * u) * 2);
-        T* ea = reinterpret_cast<T*>(&a);
-        T* eb = reinterpret_cast<T*>(&b);
+    const int per = units * groups, pairs8 = A.rotary / 16;
+    const int lt = threadIdx.x / per;
+    const int64_t t = (int64_t)blockIdx.x * tokens_per_block + lt;
+    if (lt >= tokens_per_block || t >= A.tokens) return;
+    const T* xt = static_cast<const T*>(A.x) + t * A.x_token;
+    T* yt = static_cast<T*>(A.y) + t * A.y_token;
+    const int64_t pos = min(max((int64_t)A.positions[t], (int64_t)0), A.n_positions - 1);
+    for (int w = threadIdx.x - lt * per; w < per; w += kThreads) {
+        const int h0 = w / units, u = w - h0 * units;
+        const bool turn = u < pairs8;
+        const int rest = (A.dim - A.rotary) / 8, apart = turn ? pairs8 : (rest + 1) / 2;
+        const int ia = 8 * (turn ? u : 2 * pairs8 + u - pairs8), ib = ia + 8 * apart;
+        const bool two = turn || ib < A.dim;  // an odd piece is left over behind the turned part
+        float4 cs[4];  // cos, sin of 8 pairs
+        if (turn) {
+            const float4* table = reinterpret_cast<const float4*>(A.table + pos * A.rotary);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // pairs 2k, 2k + 1
-            const float4 c = __ldg(cs + k);
-            const float s0 = A.inverse ? -c.y : c.y, s1 = A.inverse ? -c.w : c.w;
-            if (A.interleaved) {
-                T* e = (k < 2) ? ea + 4 * k : eb + 4 * (k - 2);
-                rope_turn(e[0], e[1], c.x, s0);
-                rope_turn(e[2], e[3], c.z, s1);
-            } else {
-                rope_turn(ea[2 * k], eb[2 * k], c.x, s0);
-                rope_turn(ea[2 * k + 1], eb[2 * k + 1], c.z, s1);
+            for (int k = 0; k < 4; ++k) {
+                cs[k] = __ldg(table + (A.interleaved ? 2 * u + (k & 1) + (k >> 1) * 2 * pairs8 : 4 * u + k));
+                if (A.inverse) {
+                    cs[k].y = -cs[k].y;
+                    cs[k].w = -cs[k].w;
+                }
             }
         }
-        store8(y + ia, a);
-        store8(y + ib, b);
+        for (int h = h0; h < A.heads; h += kBatch * groups) {
+            Vec8<T> a[kBatch], b[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (h + k * groups < A.heads) {
+                    const T* x = xt + (h + k * groups) * A.x_head;
+                    a[k] = load8(x + ia);
+                    if (two) b[k] = load8(x + ib);
+                }
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (h + k * groups >= A.heads) break;
+                T* ea = reinterpret_cast<T*>(&a[k]);
+                T* eb = reinterpret_cast<T*>(&b[k]);
+                if (turn) {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        if (A.interleaved) {
+                            T* e = (p < 2) ? ea + 4 * p : eb + 4 * (p - 2);
+                            rope_turn(e[0], e[1], cs[p].x, cs[p].y);
+                            rope_turn(e[2], e[3], cs[p].z, cs[p].w);
+                        } else {
+                            rope_turn(ea[2 * p], eb[2 * p], cs[p].x, cs[p].y);
+                            rope_turn(ea[2 * p + 1], eb[2 * p + 1], cs[p].z, cs[p].w);
+                        }
+                    }
+                }
+                T* y = yt + (h + k * groups) * A.y_head;
+                store8(y + ia, a[k]);
+                if (two) store8(y + ib, b[k]);
+            }
+        }
     }
 }
 
@@ -104,16 +135,19 @@ cudaError_t launch_rope_table(const double* inv_freq, int n_freq, double magnitu
 
 cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t s)
 {
-    const int units = a.rotary / 16 + (a.copy_rest ? (a.dim - a.rotary) / 8 : 0);
-    const int64_t total = a.tokens * a.heads * units;
-    const int64_t want = (total + kThreads - 1) / kThreads, cap = (int64_t)device_sm_count() * 64;
-    const int grid = (int)(want < cap ? want : cap);
+    const int units = a.rotary / 16 + (a.copy_rest ? ((a.dim - a.rotary) / 8 + 1) / 2 : 0);
+    // heads a thread does in turn: 8 where that leaves every SM 1024 threads, else fewer
+    const int64_t spare = a.tokens * a.heads * units / ((int64_t)device_sm_count() * 1024);
+    const int each = spare >= 8 ? 8 : spare >= 4 ? 4 : spare >= 2 ? 2 : 1;
+    const int groups = (a.heads + each - 1) / each, per = units * groups;
+    const int tokens_per_block = per < kThreads ? kThreads / per : 1;
+    const unsigned grid = (unsigned)((a.tokens + tokens_per_block - 1) / tokens_per_block);
     if (dtype == ECCO_BF16)
-        rope_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a, units, total);
+        rope_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a, units, groups, tokens_per_block);
     else if (dtype == ECCO_F16)
-        rope_kernel<__half><<<grid, kThreads, 0, s>>>(a, units, total);
+        rope_kernel<__half><<<grid, kThreads, 0, s>>>(a, units, groups, tokens_per_block);
     else
-        rope_kernel<float><<<grid, kThreads, 0, s>>>(a, units, total);
+        rope_kernel<float><<<grid, kThreads, 0, s>>>(a, units, groups, tokens_per_block);
     return cudaGetLastError();
 }
 
