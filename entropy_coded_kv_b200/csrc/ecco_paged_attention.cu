@@ -12,7 +12,11 @@ namespace ecco {
 namespace {
 
 constexpr int kTile = 128;                     // tokens of a scratch tile
-constexpr int kTileBytes = kTile * kG * 2;     // one head's K (or V) of a tile
+// One head's K (or V) of a tile: two halves of 64 values, 128 bytes a row, the
+// eight 16-byte pieces of a row XOR-ed with the row's low three bits -- the
+// 128-byte swizzle that the tensor cores read, so a tile goes to shared memory
+// as one contiguous copy.
+constexpr int kTileBytes = kTile * kG * 2;
 constexpr int64_t kRoundBytes = (int64_t)1 << 30;
 
 // What the device-side arrays say of one sequence, bounded.
@@ -90,15 +94,6 @@ __device__ __forceinline__ int find_seq(const int* v, int n, int x)
     return b;
 }
 
-// Byte offset of 16-byte piece c (0..15) of row r in a tile: two halves of 64
-// values, 128 bytes a row, the 8 pieces of a row XOR-ed with the row's low
-// bits -- the 128-byte swizzle that the tensor cores read, so a tile goes to
-// shared memory as one contiguous copy.
-__device__ __forceinline__ uint32_t tile_offset(int r, int c)
-{
-    return (uint32_t)((c >> 3) * (kTileBytes / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
 // ------------------------------------------------------------ barriers, copies, launches
 constexpr uint32_t kSpinLimit = 1u << 20;
 __device__ unsigned int g_timeouts = 0;
@@ -129,11 +124,23 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// A wait that gives up counts itself, raises the host-visible flag and marks
+// the CTA dead, so that its other waits end too.
+__device__ __noinline__ void wait_gave_up(volatile uint32_t* dead, int* flag)
+{
+    *dead = 1u;
+    atomicAdd(&g_timeouts, 1u);
+    if (flag) {
+        *reinterpret_cast<volatile int*>(flag) = 1;
+        __threadfence_system();
+    }
+}
+
 // Waits for the phase of the given parity: at most kSpinLimit polls of up to a
-// microsecond.  A wait that gives up counts itself, raises the host-visible
-// flag and marks the CTA dead, so that its other waits end too.
+// microsecond.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* dead, int* flag)
 {
+#pragma unroll 1
     for (uint32_t i = 0; i < kSpinLimit; ++i) {
         uint32_t done;
         asm volatile(
@@ -146,12 +153,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
         if (done) return true;
         if (*dead) return false;
     }
-    *dead = 1u;
-    atomicAdd(&g_timeouts, 1u);
-    if (flag) {
-        *reinterpret_cast<volatile int*>(flag) = 1;
-        __threadfence_system();
-    }
+    wait_gave_up(dead, flag);
     return false;
 }
 
@@ -333,7 +335,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
 // with fewer ("thin") both have the same rows, engine i the key tiles i, i + 2,
 // .. of the part, and engine 0 joins the two.  Warps 0-3 and 4-7 are the
 // engines' softmax, a thread a row = a TMEM lane; warp 8 issues the products,
-// warp 9 the copies (a tile is one 32 KB bulk copy).
+// warp 9 the copies (a tile is one 32 KB bulk copy), warp 10 works out the
+// share's parts and hands them to the others.
 // The maximum m is only moved, and O rescaled, when a row's new maximum is
 // above it by more than 2^8: until then the weights stay below 2^8 and sum and
 // products are as exact as with the true maximum.
@@ -357,24 +360,24 @@ struct AttnArgs {
 };
 
 constexpr int kRows = 256;               // rows of an item
-constexpr int kAttnThreads = 384;
+constexpr int kAttnThreads = 352;        // 8 softmax warps, products, copies, plan
 constexpr int kStages = 4;               // K and V tiles in flight
+constexpr int kParts = 4;                // parts planned ahead
 constexpr int kMaxCtas = 160;            // shares (and twice as many slots) at most
-constexpr int kBars = 2 * kStages + 13;
+constexpr int kBars = 2 * kStages + 2 * kParts + 13;
 constexpr size_t kOffRing = 2 * kTileBytes;
 constexpr size_t kOffBars = kOffRing + (size_t)kStages * kTileBytes;
-constexpr size_t kOffUnits = kOffBars + kBars * 8 + 24 + 1024;
-constexpr size_t kOffSeq = (kOffUnits + (ECCO_MAX_BATCH + 1) * 8 + 15) / 16 * 16;
-constexpr size_t kAttnSmem = 1024 + kOffSeq + sizeof(int) * (5 * ECCO_MAX_BATCH + 1);
-// Registers a thread: 384 threads start with 168 (65,536 / 384, in eights);
-// the softmax warps take 216, the other warpgroup gives up 96 of its 168:
-// 256 * 216 + 128 * 72 = 64,512 = 384 * 168.
-constexpr int kSoftRegs = 216, kIssueRegs = 72;
-static_assert(256 * kSoftRegs + 128 * kIssueRegs <= kAttnThreads * 168, "more registers than the block was launched with");
+constexpr size_t kOffParts = kOffBars + (kBars * 8 + 8 + 15) / 16 * 16;  // the barriers, tensor-memory address, dead mark
+constexpr size_t kOffMl = kOffParts + kParts * 48;                       // engine 1's maxima and sums, for engine 0
+constexpr size_t kOffSeq = kOffMl + 256 * sizeof(float);
+constexpr size_t kOffUnits = kOffSeq + 16 * ECCO_MAX_BATCH;
+constexpr size_t kOffTile = kOffUnits + 8 * (ECCO_MAX_BATCH + 1);
+constexpr size_t kAttnSmem = 1024 + kOffTile + 4 * ECCO_MAX_BATCH;
 
 // D fp32, A and B bf16, N = 128, M = 128; kIdescPV: B N-major (bit 16).
 constexpr uint32_t kIdescQK = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+constexpr uint32_t kNegateA = 1u << 13;  // for a negative scale
 
 // Shared-memory matrix descriptor with the 128-byte swizzle (layout type 2):
 // 8-row groups 1024 bytes apart; leading offset = the distance between the
@@ -388,14 +391,14 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr)
 // The issuing warp runs as a whole (`leader` is true in one lane), so that the
 // operands stay in uniform registers: issued from a branch of one lane, the
 // eight products of a tile took 600 cycles to issue, more than they run.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate, uint32_t leader)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate, uint32_t leader)
 {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 q, %5, 0;\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(kIdescQK), "r"(accumulate), "r"(leader)
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
@@ -529,12 +532,15 @@ __device__ __forceinline__ Span span_of(const Seq& s, int group, int window, int
     return r;
 }
 
-struct Plan {  // in shared memory, at `at`
+// Units that a key tile of the span costs.
+__device__ __forceinline__ int tile_cost(const Span& r) { return r.rows > 128 ? 2 : 1; }
+
+// What the planning warp keeps in shared memory.
+struct Plan {
     uint8_t* at;
-    int batch, tiles;
-    __device__ __forceinline__ long long* units() const { return reinterpret_cast<long long*>(at + kOffUnits); }  // [batch + 1] units before sequence b, over the round's heads
     __device__ __forceinline__ int4* seqs() const { return reinterpret_cast<int4*>(at + kOffSeq); }
-    __device__ __forceinline__ int* tile() const { return reinterpret_cast<int*>(at + kOffSeq + 16 * ECCO_MAX_BATCH); }  // scratch tile of (head 0, key tile 0) of sequence b
+    __device__ __forceinline__ long long* units() const { return reinterpret_cast<long long*>(at + kOffUnits); }  // before sequence b, over the round's heads
+    __device__ __forceinline__ int* tile() const { return reinterpret_cast<int*>(at + kOffTile); }  // scratch tile of (head 0, key tile 0) of sequence b
     __device__ __forceinline__ Seq seq(int b) const
     {
         const int4 v = seqs()[b];
@@ -542,82 +548,178 @@ struct Plan {  // in shared memory, at `at`
     }
 };
 
-// Units that a key tile of the span costs.
-__device__ __forceinline__ int tile_cost(const Span& r) { return r.rows > 128 ? 2 : 1; }
-
-// One part of an item: key tiles [t0, t0 + n) of its rows.
+// One part of an item, as the planning warp hands it to the others: key tiles
+// [t0, t0 + n) of rows g0 .. g0 + rows - 1 (row = new token * group + query head
+// of the group).
 struct Part {
-    int b, h, qt, rows, t0, n;
-    bool begins, ends;  // the item's first / last tiles are among them
-    long long last;     // the item's last unit
+    int q0, base, keys, g0;  // the sequence's first token row, position of new token 0, keys; first row
+    int rows, t0, n, ends;   // rows = 0: no part follows; ends: 1 the item begins in this part, 2 it ends in it
+    int tile_k, tile_v, h;   // scratch tiles of key tile t0, head of the round
     __device__ __forceinline__ bool thin() const { return rows <= 128; }
     __device__ __forceinline__ int row0(int i) const { return thin() ? 0 : 128 * i; }  // of engine i's tile
     __device__ __forceinline__ int tiles(int i) const { return thin() ? (n + 1 - i) >> 1 : n; }
-    __device__ __forceinline__ bool active(int i) const { return tiles(i) > 0; }
 };
 
-// Walks a share's parts.  Every warp runs its own copy.  A tile belongs to the
-// share that holds its last unit.
-struct Walk {
-    const Plan& P;
-    int group, window, hn;
-    long long item, stop;  // first unit of the item, end of the share
-    int b, h, qt, skip;    // the item, and its tiles before the share
-
-    __device__ __forceinline__ bool next(Part& x)
-    {
-        if (item >= stop) return false;
-        Seq s = P.seq(b);
-        while (qt * kRows >= s.q * group) {  // the sequence's rows are done: its next head, or the next sequence with rows
-            qt = 0;
-            if (s.q > 0 && ++h < hn) break;
-            h = 0;
-            s = P.seq(++b);
+// The planning warp: works out the shares and hands this CTA's parts on.
+__device__ void plan_parts(const AttnArgs& A, uint8_t* smem, uint32_t bar_part, uint32_t bar_taken, volatile uint32_t* dead, int lane)
+{
+    const Plan P{smem};
+    const int batch = A.p.batch, group = A.group, window = A.w.window;
+    int tiles = 0;
+    long long total = 0;
+    for (int b0 = 0; b0 < batch; b0 += 32) {
+        const int b = b0 + lane;
+        Seq s{0, 0, 0, 0};
+        if (b < batch) s = seq_of(A.p, A.w, b);
+        int first, count;
+        seq_tiles(s, window, first, count);
+        const int nq = (s.q * group + kRows - 1) / kRows;  // items of a head
+        long long u = 0;
+        if (nq == 1) {
+            const Span r = span_of(s, group, window, 0);
+            u = max(1, r.n) * tile_cost(r);
         }
-        const Span r = span_of(s, group, window, qt);
-        const int units = max(1, r.n), cost = tile_cost(r);
-        const int until = (int)min((long long)units, (stop - item) / cost);
-        if (until <= skip) return false;
-        x.b = b;
-        x.h = h;
-        x.qt = qt;
-        x.rows = r.rows;
-        x.t0 = r.t0 + skip;
-        x.n = min(until, r.n) - skip;
-        x.begins = skip == 0;
-        x.ends = until == units;
-        x.last = item + (long long)units * cost - 1;
-        item += (long long)units * cost;
-        skip = 0;
-        ++qt;
-        return true;
+        for (uint32_t m = __ballot_sync(0xffffffffu, nq > 1); m; m &= m - 1) {  // longer ones, the warp together
+            const int from = __ffs(m) - 1, n = __shfl_sync(0xffffffffu, nq, from);
+            const Seq z{0, __shfl_sync(0xffffffffu, s.q, from), __shfl_sync(0xffffffffu, s.base, from),
+                        __shfl_sync(0xffffffffu, s.keys, from)};
+            long long w = 0;
+            for (int qt = lane; qt < n; qt += 32) {
+                const Span r = span_of(z, group, window, qt);
+                w += max(1, r.n) * tile_cost(r);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+            if (lane == from) u = w;
+        }
+        u *= A.hn;
+        int ct = count;
+        long long cu = u;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, ct, d);
+            const long long v = __shfl_up_sync(0xffffffffu, cu, d);
+            if (lane >= d) {
+                ct += t;
+                cu += v;
+            }
+        }
+        if (b < batch) {
+            P.seqs()[b] = make_int4(s.q0, s.q, s.base, s.keys);
+            P.units()[b] = total + cu - u;
+            P.tile()[b] = tiles + ct - count - first;
+        }
+        tiles += __shfl_sync(0xffffffffu, ct, 31);
+        total += __shfl_sync(0xffffffffu, cu, 31);
     }
-};
+    if (lane == 0) P.units()[batch] = total;
+    __syncwarp();
+
+    // shares of two units at least: each holds a tile's last
+    const long long shares = min((long long)gridDim.x, max(1ll, total / 2));
+    int4 cut = make_int4(0, -1, 0, 0);
+    uint32_t slot = 0;
+    bool ok = true;
+    auto hand = [&](const int4& a, const int4& b, const int4& c) {
+        const uint32_t i = slot % kParts, use = slot / kParts;
+        if (use > 0 && ok) ok = mbar_wait(bar_taken + 8 * i, (use - 1) & 1, dead, A.flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && lane == 0) {
+            int4* d = reinterpret_cast<int4*>(smem + kOffParts + 48 * i);
+            d[0] = a;
+            d[1] = b;
+            d[2] = c;
+            mbar_arrive(bar_part + 8 * i);
+        }
+        ++slot;
+    };
+    if (total > 0 && blockIdx.x < shares) {
+        const long long u0 = total * blockIdx.x / shares, stop = total * (blockIdx.x + 1) / shares;
+        int b = 0, top = batch - 1;  // the sequence of unit u0: the last that begins at or before it
+        while (b < top) {
+            const int mid = (b + top + 1) >> 1;
+            if (P.units()[mid] <= u0)
+                b = mid;
+            else
+                top = mid - 1;
+        }
+        Seq s = P.seq(b);
+        long long rem = u0 - P.units()[b];
+        const long long per_head = (P.units()[b + 1] - P.units()[b]) / A.hn;
+        int h = 0, qt = 0;
+        while (rem >= per_head) {
+            rem -= per_head;
+            ++h;
+        }
+        const int n = (s.q * group + kRows - 1) / kRows;
+        for (int q = 0; q < n; q += 32) {  // the item: 32 at a time
+            Span r{0, 0, 0};
+            if (q + lane < n) r = span_of(s, group, window, q + lane);
+            const long long x = q + lane < n ? max(1, r.n) * tile_cost(r) : 0;
+            long long sum = x;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += t;
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, sum > rem);
+            if (m) {
+                qt = q + __ffs(m) - 1;
+                rem -= __shfl_sync(0xffffffffu, sum - x, __ffs(m) - 1);
+                break;
+            }
+            rem -= __shfl_sync(0xffffffffu, sum, 31);
+        }
+        long long item = u0 - rem;  // its first unit
+        int skip = -1;              // its tiles before the share: from `rem`, once its cost is known
+        while (item < stop && ok) {
+            while (qt * kRows >= s.q * group) {  // the rows are done: the next head, or the next sequence with rows
+                qt = 0;
+                if (s.q > 0 && ++h < A.hn) break;
+                h = 0;
+                s = P.seq(++b);
+            }
+            const Span r = span_of(s, group, window, qt);
+            const int units = max(1, r.n), cost = tile_cost(r);
+            if (skip < 0) skip = (int)rem / cost;
+            const int until = (int)min((long long)units, (stop - item) >> (cost - 1));  // cost 1 or 2
+            if (until <= skip) break;
+            const int begins = skip == 0, ends = until == units;
+            const int tile = h * tiles + P.tile()[b] + r.t0 + skip;
+            hand(make_int4(s.q0, s.base, s.keys, qt * kRows), make_int4(r.rows, r.t0 + skip, min(until, r.n) - skip, begins | ends << 1),
+                 make_int4(tile, tile + A.hn * tiles, h, 0));
+            if (begins && !ends)
+                cut = make_int4(b, h, qt, (int)(((item + (long long)units * cost) * shares - 1) / total));
+            item += (long long)units * cost;
+            skip = 0;
+            ++qt;
+        }
+    }
+    hand(make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0));
+    launch_dependents();  // no earlier: the joining CTAs would sit on the SMs meanwhile
+    if (lane == 0) A.part_item[blockIdx.x] = cut;
+}
 
 __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const __grid_constant__ AttnArgs A)
 {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ long long s_item;  // first unit of the share's first item
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
     const uint32_t bars = smem_u32(smem + kOffBars);
-    const uint32_t bar_full = bars, bar_empty = bars + 8 * kStages, bar_q = bars + 16 * kStages, bar_s = bar_q + 16,
-                   bar_p = bar_s + 16, bar_o = bar_p + 32, bar_x = bar_o + 16, bar_end = bar_x + 16;
+    const uint32_t bar_full = bars, bar_empty = bar_full + 8 * kStages;            // ring tiles: landed, free
+    const uint32_t bar_part = bar_empty + 8 * kStages, bar_taken = bar_part + 8 * kParts;
+    const uint32_t bar_q = bar_taken + 8 * kParts, bar_s = bar_q + 16, bar_p = bar_s + 16;  // [engine]; weights: [piece][engine]
+    const uint32_t bar_o = bar_p + 32, bar_x = bar_o + 16, bar_end = bar_x + 16;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffBars + kBars * 8);
     volatile uint32_t* dead = s_tmem + 1;
-    int* s_start = reinterpret_cast<int*>(s_tmem + 2);  // b, h, qt, skip of the share's first unit
-    float* s_ml = reinterpret_cast<float*>(s_start + 4);  // engine 1's maxima and sums of a thin part, for engine 0
-    Plan P;
-    P.at = smem;
-    P.batch = A.p.batch;
+    float* s_ml = reinterpret_cast<float*>(smem + kOffMl);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int window = A.w.window;
-    launch_dependents();
 
-    // ---- plan
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(bar_full + 8 * i, 1);
-            mbar_init(bar_empty + 8 * i, 1);
+        for (int i = 0; i < 2 * kStages; ++i) mbar_init(bar_full + 8 * i, 1);
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(bar_part + 8 * i, 1);
+            mbar_init(bar_taken + 8 * i, 10);  // the softmax warps, products and copies
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_q + 8 * i, 128);
@@ -636,129 +738,46 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    for (int b = tid; b < P.batch; b += kAttnThreads) {
-        const Seq s = seq_of(A.p, A.w, b);
-        int first, count;
-        seq_tiles(s, window, first, count);
-        P.seqs()[b] = make_int4(s.q0, s.q, s.base, s.keys);
-        P.tile()[b] = count;
-    }
-    __syncthreads();
-    for (int b = warp; b < P.batch; b += kAttnThreads / 32) {
-        const Seq s = P.seq(b);
-        const int n = (s.q * A.group + kRows - 1) / kRows;
-        long long u = 0;
-        for (int qt = lane; qt < n; qt += 32) {
-            const Span r = span_of(s, A.group, window, qt);
-            u += max(1, r.n) * tile_cost(r);
-        }
-#pragma unroll
-        for (int d = 16; d; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
-        if (lane == 0) P.units()[b] = u * A.hn;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        long long run = 0;
-        for (int i0 = 0; i0 < P.batch; i0 += 32) {
-            const int i = i0 + lane;
-            const long long x = i < P.batch ? P.units()[i] : 0;
-            long long s = x;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, s, d);
-                if (lane >= d) s += t;
-            }
-            if (i < P.batch) P.units()[i] = run + s - x;
-            run += __shfl_sync(0xffffffffu, s, 31);
-        }
-        if (lane == 0) P.units()[P.batch] = run;
-    } else if (warp == 1) {
-        warp_prefix(P.tile(), P.batch, lane);
-    }
-    __syncthreads();
-    P.tiles = P.tile()[P.batch];
-    const long long total = P.units()[P.batch];
-    const long long shares = min((long long)gridDim.x, max(1ll, total / 2));  // of two units at least: each holds a tile's last
-    const bool works = total > 0 && blockIdx.x < shares;
-    const long long u0 = works ? total * blockIdx.x / shares : 0, u1 = works ? total * (blockIdx.x + 1) / shares : 0;
-    __syncthreads();
-    for (int b = tid; b < P.batch; b += kAttnThreads) {
-        int first, count;
-        seq_tiles(P.seq(b), window, first, count);
-        P.tile()[b] -= first;
-    }
-    if (warp == 0 && u0 < u1) {  // the item of the share's first unit
-        int b = 0, top = P.batch - 1;
-        while (b < top) {
-            const int mid = (b + top + 1) >> 1;
-            if (P.units()[mid] <= u0)
-                b = mid;
-            else
-                top = mid - 1;
-        }
-        const Seq s = P.seq(b);
-        const long long per_head = (P.units()[b + 1] - P.units()[b]) / A.hn;
-        long long rem = u0 - P.units()[b];
-        const int h = (int)(rem / per_head);
-        rem -= h * per_head;
-        const int n = (s.q * A.group + kRows - 1) / kRows;
-        for (int q0 = 0; q0 < n; q0 += 32) {
-            const int qt = q0 + lane;
-            Span r{0, 0, 0};
-            if (qt < n) r = span_of(s, A.group, window, qt);
-            const int x = qt < n ? max(1, r.n) * tile_cost(r) : 0;
-            long long sum = x;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, sum, d);
-                if (lane >= d) sum += t;
-            }
-            const uint32_t m = __ballot_sync(0xffffffffu, sum > rem);
-            if (m) {
-                if (lane == __ffs(m) - 1) {
-                    s_start[0] = b;
-                    s_start[1] = h;
-                    s_start[2] = qt;
-                    s_start[3] = (int)(rem - (sum - x)) / tile_cost(r);
-                    s_item = u0 - (rem - (sum - x));
-                }
-                break;
-            }
-            rem -= __shfl_sync(0xffffffffu, sum, 31);
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    Walk W{P, A.group, window, A.hn, works ? s_item : 0, u1, s_start[0], s_start[1], s_start[2], s_start[3]};
-    const int64_t v_offset = (int64_t)A.hn * P.tiles * kTileBytes;
+
+    bool ok = true;
+    uint32_t taken = 0;
+    auto take = [&]() -> Part {  // the next part; rows = 0 after the last, or if the CTA gave up
+        const uint32_t i = taken % kParts;
+        if (ok) ok = mbar_wait(bar_part + 8 * i, (taken / kParts) & 1, dead, A.flag);
+        ++taken;
+        const int4* d = reinterpret_cast<const int4*>(smem + kOffParts + 48 * i);
+        const int4 a = d[0], b = d[1], c = d[2];
+        return Part{a.x, a.y, a.z, a.w, ok ? b.x : 0, b.y, b.z, b.w, c.x, c.y, c.z};
+    };
+    auto give_back = [&]() { mbar_arrive(bar_taken + 8 * ((taken - 1) % kParts)); };  // one lane, once the part is in registers
 
     // The ring's tiles, in the order in which the products take them: wide parts
     // K_0 V_0 K_1 V_1 .., thin ones K_0 K_1 V_0 K_2 V_1 K_3 ..
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 9 && lane == 0) {
+    if (warp == 10) {
+        plan_parts(A, smem, bar_part, bar_taken, dead, lane);
+    } else if (warp == 9) {
+        if (lane == 0) {
             // ---- copies
-            after_previous();  // the tiles are decoded
-            Part x;
             uint32_t n = 0;
-            bool ok = true;
-            while (ok && W.next(x)) {
-                const uint8_t* src = A.scratch + ((int64_t)x.h * P.tiles + P.tile()[x.b] + x.t0) * kTileBytes;
-                auto copy = [&](int j, bool v) {
+            after_previous();  // the tiles are decoded
+            for (;;) {
+                const Part x = take();
+                give_back();
+                if (!x.rows) break;
+                int k = 0, v = 0;
+                while (k + v < 2 * x.n) {
+                    const bool key = k < min(x.n, v + (x.thin() ? 2 : 1));
+                    const int64_t tile = key ? x.tile_k + k++ : x.tile_v + v++;
                     const uint32_t st = n % kStages, use = n / kStages;
-                    if (!ok || (use > 0 && !(ok = mbar_wait(bar_empty + 8 * st, (use - 1) & 1, dead, A.flag)))) return;
+                    if (use > 0 && ok) ok = mbar_wait(bar_empty + 8 * st, (use - 1) & 1, dead, A.flag);
+                    if (!ok) break;
                     mbar_expect(bar_full + 8 * st, kTileBytes);
-                    bulk_copy(smem_u32(smem + kOffRing) + st * kTileBytes, src + (int64_t)j * kTileBytes + (v ? v_offset : 0),
-                              kTileBytes, bar_full + 8 * st);
+                    bulk_copy(smem_u32(smem + kOffRing) + st * kTileBytes, A.scratch + tile * kTileBytes, kTileBytes, bar_full + 8 * st);
                     ++n;
-                };
-                const int ahead = x.thin() ? 2 : 1;
-                for (int j = 0; j < min(ahead, x.n); ++j) copy(j, false);
-                for (int j = 0; j < x.n && ok; ++j) {
-                    copy(j, true);
-                    if (j + ahead < x.n) copy(j + ahead, false);
                 }
             }
             // every copy has landed before the CTA ends (they have, unless it gave up)
@@ -767,249 +786,210 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                 mbar_wait(bar_full + 8 * (k % kStages), (k / kStages) & 1, &zero, nullptr);
             }
         }
-        if (warp == 8) {
-            // ---- products (the whole warp)
-            const uint32_t leader = elect_one();
-            Part x;
-            uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-            bool ok = true;
-            const uint32_t ring = smem_u32(smem + kOffRing), qs = smem_u32(smem);
-            auto wait = [&](uint32_t bar, uint32_t count) {
-                if (ok) ok = mbar_wait(bar, count & 1, dead, A.flag);
-                ok = __all_sync(0xffffffffu, ok);
-                tc_fence_after();
-            };
-            auto full = [&](uint32_t k) {  // ring tile k has landed
-                if (ok) ok = mbar_wait(bar_full + 8 * (k % kStages), (k / kStages) & 1, dead, A.flag);
-                ok = __all_sync(0xffffffffu, ok);
-            };
-            auto release = [&](uint32_t k) {
-                if (ok) mma_commit(bar_empty + 8 * (k % kStages), leader);
-            };
-            auto score = [&](int i, uint32_t k) {  // S_i = Q_i times the keys in ring tile k
-                if (!ok) return;
-                const uint64_t a = sw128_desc(qs + i * kTileBytes), b = sw128_desc(ring + (k % kStages) * kTileBytes);
-#pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const uint64_t o = (uint64_t)(((t >> 2) * (kTileBytes / 2) + (t & 3) * 32) >> 4);
-                    mma_ss(tmem + 128 * i, a + o, b + o, t > 0, leader);
+    } else if (warp == 8) {
+        // ---- products (the whole warp)
+        const uint32_t leader = elect_one();
+        const uint32_t ring = smem_u32(smem + kOffRing), qs = smem_u32(smem);
+        const uint32_t idesc = kIdescQK | (A.scale < 0.0f ? kNegateA : 0u);
+        uint32_t at = 0, np = 0, nq = 0;  // ring tiles taken; weights and queries waited for, a bit an engine (the parity)
+        auto settle = [&]() { ok = __all_sync(0xffffffffu, ok); };
+        auto full = [&](uint32_t k) {  // ring tile k has landed
+            if (ok) ok = mbar_wait(bar_full + 8 * (k % kStages), (k / kStages) & 1, dead, A.flag);
+            settle();
+        };
+        for (;;) {
+            const Part x = take();
+            settle();
+            if (lane == 0) give_back();
+            if (!x.rows || !ok) break;
+            if (x.n == 0) continue;
+            const bool thin = x.thin();
+            const int steps = thin ? x.n : 2 * x.n;
+            uint32_t v = 0, k = 0;  // ring tiles in use
+            // step e: O_i += P_i times its values, then S_i of its engine's next keys (from step -2 on: S alone)
+#pragma unroll 1
+            for (int e = -2; e < steps && ok; ++e) {
+                const int i = e & 1;
+                const bool fresh = thin || i == 0, last = thin || i == 1;  // of the engines that share the tiles
+                const bool more = (thin ? e + 2 : (e >> 1) + 1) < x.n;
+                if (fresh) {
+                    if (e >= 0) full(v = at++);
+                    if (more) full(k = at++);
                 }
-                mma_commit(bar_s + 8 * i, leader);
-            };
-            auto weigh = [&](int i, uint32_t k, bool first) {  // O_i += P_i times the values in ring tile k
-                const uint64_t b = sw128_desc(ring + (k % kStages) * kTileBytes);
-                const uint32_t count = np[i]++;
+                if (e >= 0) {
+                    const uint64_t b = sw128_desc(ring + (v % kStages) * kTileBytes);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {  // the weights of 96 keys, then of the last 32
-                    wait(bar_p + 16 * hf + 8 * i, count);
-                    if (!ok) return;
+                    for (int piece = 0; piece < 2; ++piece) {  // the weights of 96 keys, then of the last 32
+                        if (ok) ok = mbar_wait(bar_p + 16 * piece + 8 * i, (np >> i) & 1, dead, A.flag);
+                        settle();
+                        tc_fence_after();
+                        if (ok) {
 #pragma unroll
-                    for (int t = 6 * hf; t < 6 + 2 * hf; ++t)
-                        mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, b + (uint64_t)(t * 2048 >> 4), (!first || t > 0) ? 1u : 0u, leader);
-                }
-                mma_commit(bar_o + 8 * i, leader);
-            };
-            while (ok && W.next(x)) {
-                if (x.n == 0) continue;
-                if (x.thin()) {
-                    uint32_t at = n;  // next ring tile
-                    for (int i = 0; i < min(2, x.n); ++i) {
-                        wait(bar_q + 8 * i, nq[i]++);
-                        full(at);
-                        score(i, at);
-                        release(at++);
-                    }
-                    for (int j = 0; j < x.n && ok; ++j) {
-                        const int i = j & 1;
-                        full(at);
-                        if (j + 2 < x.n) full(at + 1);
-                        weigh(i, at, j < 2);
-                        release(at++);
-                        if (j + 2 < x.n) {
-                            score(i, at);
-                            release(at++);
+                            for (int t = 6 * piece; t < 6 + 2 * piece; ++t)
+                                mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, b + (uint64_t)(t * 2048 >> 4), (e > 1 || t > 0) ? 1u : 0u, leader);
                         }
                     }
-                } else {
-                    full(n);
-                    for (int i = 0; i < 2; ++i) {
-                        wait(bar_q + 8 * i, nq[i]++);
-                        score(i, n);
-                    }
-                    release(n);
-                    for (int j = 0; j < x.n && ok; ++j) {
-                        const uint32_t v = n + 2 * j + 1, k = v + 1;
-                        full(v);
-                        if (j + 1 < x.n) full(k);
-                        for (int i = 0; i < 2; ++i) {
-                            weigh(i, v, j == 0);
-                            if (i == 1) release(v);
-                            if (j + 1 < x.n) {
-                                score(i, k);
-                                if (i == 1) release(k);
-                            }
-                        }
+                    np ^= 1u << i;
+                    if (ok) {
+                        mma_commit(bar_o + 8 * i, leader);
+                        if (last) mma_commit(bar_empty + 8 * (v % kStages), leader);
                     }
                 }
-                n += 2 * x.n;
+                if (more) {
+                    if (e < 0) {
+                        if (ok) ok = mbar_wait(bar_q + 8 * i, (nq >> i) & 1, dead, A.flag);
+                        settle();
+                        nq ^= 1u << i;
+                    }
+                    if (ok) {
+                        const uint64_t a = sw128_desc(qs + i * kTileBytes), b = sw128_desc(ring + (k % kStages) * kTileBytes);
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) {
+                            const uint64_t o = (uint64_t)(((t >> 2) * (kTileBytes / 2) + (t & 3) * 32) >> 4);
+                            mma_ss(tmem + 128 * i, a + o, b + o, idesc, t > 0, leader);
+                        }
+                        mma_commit(bar_s + 8 * i, leader);
+                        if (last) mma_commit(bar_empty + 8 * (k % kStages), leader);
+                    }
+                }
             }
-            // every product issued is done before the tensor memory is freed
-            uint32_t zero = 0u;
-            mma_commit(bar_end, leader);
-            mbar_wait(bar_end, 0u, &zero, nullptr);
         }
+        // every product issued is done before the tensor memory is freed
+        uint32_t zero = 0u;
+        mma_commit(bar_end, leader);
+        mbar_wait(bar_end, 0u, &zero, nullptr);
     } else {
         // ---- softmax: a thread a row of engine i
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int i = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + 128 * i, to = tmem + lanes + 256 + 128 * i;
-        uint8_t* qs = smem + i * kTileBytes;
-        const uint32_t flip = A.scale < 0.0f ? 0x80008000u : 0u;       // a negative scale turns Q's signs
         const float c = fmaxf(fabsf(A.scale) * 1.44269504f, 1e-30f);  // 0: weights of 1, and masked scores stay -inf
         const uint64_t c2 = pair(c, c);
-        uint32_t ns = 0, no = 0, nx[2] = {0, 0};
-        bool ok = true;
-        int4 cut = make_int4(0, -1, 0, 0);
-        Part x, y;
-        auto load_q = [&](const Part& z) {  // this thread's row of Q, zeros behind the item's rows
-            const int r = z.row0(i) + row;
-            uint4 v[16];
-            if (r < z.rows) {
-                const int g = z.qt * kRows + r, tok = P.seqs()[z.b].x + g / A.group;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    A.q + (int64_t)tok * A.q_token + (int64_t)((A.h0 + z.h) * A.group + g % A.group) * A.q_head);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    v[k] = src[k];
-                    v[k] = make_uint4(v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) *reinterpret_cast<uint4*>(qs + tile_offset(row, k)) = v[k];
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            mbar_arrive(bar_q + 8 * i);
-        };
+        uint32_t ns = 0, no = 0, nx = 0;
+        Part x{};
+        float m = -INFINITY, l = 0.0f;  // the row's maximum and sum, over the part so far
         auto wait = [&](uint32_t bar, uint32_t count) {  // the whole warp: tensor-memory instructions follow
             if (ok) ok = mbar_wait(bar, count & 1, dead, A.flag);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
         };
-        float m = -INFINITY, l = 0.0f;  // the row's maximum and sum, over the part so far
-        auto finish = [&]() {            // part x is done: its rows of the output, or of the part's slot
-            const int r = x.row0(i) + row, g = x.qt * kRows + r, n = x.tiles(i);
-            const bool both = x.thin() && x.n > 1;  // a thin part on both engines
-            const bool real = r < x.rows, idle = x.row0(i) + (warp & 3) * 32 >= x.rows;
-            if (n > 0) wait(bar_o + 8 * i, no - 1);
-            if (both && i == 1) {  // O_1 stays in tensor memory until engine 0 has read it
-                s_ml[row] = m;
-                s_ml[128 + row] = l;
-                tc_fence_before();
-                mbar_arrive(bar_x);
-                ++nx[1];
-            } else if (x.row0(i) < x.rows && (i == 0 || !x.thin())) {
-                float f0 = 1.0f, f1 = 0.0f;
-                if (both) {
-                    wait(bar_x, nx[0]++);
-                    const float m1 = s_ml[row], l1 = s_ml[128 + row], mn = fmaxf(m, m1);
-                    f0 = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
-                    f1 = m1 == -INFINITY ? 0.0f : ex2((m1 - mn) * c);
-                    l = l * f0 + l1 * f1;
-                    m = mn;
-                }
-                const bool whole = x.begins && x.ends;
-                const int64_t slot = 2 * (int64_t)blockIdx.x + (x.begins ? 1 : 0);
-                const int64_t at = (int64_t)P.seqs()[x.b].x + (real ? g / A.group : 0);
-                const int qh = (A.h0 + x.h) * A.group + g % A.group;
-                if (whole) {
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    f0 *= inv;
-                    f1 *= inv;
-                }
-                if (!idle) {
-#pragma unroll 1
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[32], o1[32];
-                        __syncwarp();
-                        if (n > 0) {
-                            tmem_ld32(to + 32 * k, o);
-                            if (both) tmem_ld32(to + 128 + 32 * k, o1);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int t = 0; t < 32; ++t) {
-                                const float e = __uint_as_float(o[t]) * f0;
-                                o[t] = __float_as_uint(both ? fmaf(__uint_as_float(o1[t]), f1, e) : e);
-                            }
-                        } else {  // the row sees no key
-#pragma unroll
-                            for (int t = 0; t < 32; ++t) o[t] = 0u;
-                        }
-                        if (!ok || !real) {
-                        } else if (whole) {
-                            uint4* dst = reinterpret_cast<uint4*>(A.out + at * A.out_token + (int64_t)qh * A.out_head) + 4 * k;
-#pragma unroll
-                            for (int t = 0; t < 4; ++t) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    w[e] = pack_bf16x2(__uint_as_float(o[8 * t + 2 * e]), __uint_as_float(o[8 * t + 2 * e + 1]));
-                                dst[t] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        } else {
-                            uint4* dst = reinterpret_cast<uint4*>(A.part_o) + (slot * 32 + 8 * k) * A.slot_rows + r;
-#pragma unroll
-                            for (int t = 0; t < 8; ++t)
-                                dst[t * A.slot_rows] = make_uint4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
-                        }
-                    }
-                    if (ok && real) {
-                        if (whole) {
-                            if (A.lse)
-                                A.lse[at * A.p.kv_heads * A.group + qh] =
-                                    l == 0.0f ? -INFINITY : fmaf(m, c * 0.69314718f, logf(l));
-                        } else {
-                            A.part_ml[(slot * 2) * A.slot_rows + r] = m == -INFINITY ? -INFINITY : m * c;
-                            A.part_ml[(slot * 2 + 1) * A.slot_rows + r] = l;
-                        }
-                    }
-                    __syncwarp();
-                }
-                tc_fence_before();  // O is read before the next part's first product is allowed in
-                if (both) mbar_arrive(bar_x + 8);
-            }
-            if (x.begins && !x.ends) cut = make_int4(x.b, x.h, x.qt, (int)(((x.last + 1) * shares - 1) / total));
-        };
         // one pass more than parts: Q of the next part is loaded, and its first
         // products can start, before this one's output is written
         for (bool have = false;; have = true) {
-            const bool has = W.next(y);
-            if (has && y.active(i)) load_q(y);  // the scores that read the last Q are done
-            if (have) finish();
-            if (!has) break;
+            Part y = take();
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) y.rows = 0;
+            if (lane == 0) give_back();
+            if (y.rows && y.tiles(i) > 0) {  // this thread's row of Q, zeros behind the item's rows (the scores that read the last Q are done)
+                const int r = y.row0(i) + row, g = y.g0 + r, tok = g / A.group;
+                const uint32_t live = r < y.rows ? 16u : 0u;
+                const uint16_t* src = A.q;
+                if (live) src += (int64_t)(y.q0 + tok) * A.q_token + (int64_t)((A.h0 + y.h) * A.group + g - tok * A.group) * A.q_head;
+                const uint32_t dst = smem_u32(smem) + i * kTileBytes + row * 128;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                     dst + (k >> 3) * (kTileBytes / 2) + (((k & 7) ^ (row & 7)) << 4)),
+                                 "l"(src + 8 * k), "r"(live)
+                                 : "memory");
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(bar_q + 8 * i);
+            }
+            if (have) {
+                // ---- part x is done: its rows of the output, or of the part's slot
+                const int r = x.row0(i) + row, g = x.g0 + r, n = x.tiles(i), tok = g / A.group;
+                const bool both = x.thin() && x.n > 1;  // a thin part on both engines
+                const bool real = r < x.rows, idle = x.row0(i) + (warp & 3) * 32 >= x.rows;
+                if (n > 0) wait(bar_o + 8 * i, no - 1);
+                if (both && i == 1) {  // O_1 stays in tensor memory until engine 0 has read it
+                    s_ml[row] = m;
+                    s_ml[128 + row] = l;
+                    tc_fence_before();
+                    mbar_arrive(bar_x);
+                    ++nx;
+                } else if (i == 0 || !x.thin()) {
+                    float f0 = 1.0f, f1 = 0.0f;
+                    if (both) {
+                        wait(bar_x, nx++);
+                        const float m1 = s_ml[row], l1 = s_ml[128 + row], mn = fmaxf(m, m1);
+                        f0 = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
+                        f1 = m1 == -INFINITY ? 0.0f : ex2((m1 - mn) * c);
+                        l = l * f0 + l1 * f1;
+                        m = mn;
+                    }
+                    const bool whole = x.ends == 3;
+                    const int64_t slot = 2 * (int64_t)blockIdx.x + (x.ends & 1);
+                    const int qh = (A.h0 + x.h) * A.group + g - tok * A.group;
+                    const int64_t at = (int64_t)x.q0 + tok;
+                    if (whole) {
+                        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                        f0 *= inv;
+                        f1 *= inv;
+                    }
+                    if (!idle) {
+                        uint4* out = reinterpret_cast<uint4*>(A.out + at * A.out_token + (int64_t)qh * A.out_head);
+                        uint4* part = reinterpret_cast<uint4*>(A.part_o) + slot * 32 * A.slot_rows + r;
+#pragma unroll 1
+                        for (int k = 0; k < 128; k += 16) {
+                            uint32_t o[16], o1[16];
+                            __syncwarp();
+                            if (n > 0) tmem_ld16(to + k, o);
+                            if (both) tmem_ld16(to + 128 + k, o1);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int t = 0; t < 16; ++t) {
+                                const float e = n > 0 ? __uint_as_float(o[t]) * f0 : 0.0f;  // n = 0: the row sees no key
+                                o[t] = __float_as_uint(both ? fmaf(__uint_as_float(o1[t]), f1, e) : e);
+                            }
+                            if (ok && real) {
+                                if (whole) {
+#pragma unroll
+                                    for (int t = 0; t < 8; ++t)
+                                        o[t] = pack_bf16x2(__uint_as_float(o[2 * t]), __uint_as_float(o[2 * t + 1]));
+                                    out[k / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+                                    out[k / 8 + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+                                } else {
+#pragma unroll
+                                    for (int t = 0; t < 4; ++t)
+                                        part[(int64_t)(k / 4 + t) * A.slot_rows] = make_uint4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
+                                }
+                            }
+                        }
+                        if (ok && real) {
+                            if (whole) {
+                                if (A.lse)
+                                    A.lse[at * A.p.kv_heads * A.group + qh] = l == 0.0f ? -INFINITY : fmaf(m, c * 0.69314718f, logf(l));
+                            } else {
+                                A.part_ml[(slot * 2) * A.slot_rows + r] = m == -INFINITY ? -INFINITY : m * c;
+                                A.part_ml[(slot * 2 + 1) * A.slot_rows + r] = l;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    tc_fence_before();  // O is read before the next part's first product is allowed in
+                    if (both) mbar_arrive(bar_x + 8);
+                }
+            }
+            if (!y.rows) break;
             x = y;
             const int r = x.row0(i) + row, n = x.tiles(i), step = x.thin() ? 2 : 1;
-            const Seq s = P.seq(x.b);
+            const Seq s{x.q0, 0, x.base, x.keys};
             const bool real = r < x.rows, idle = x.row0(i) + (warp & 3) * 32 >= x.rows;  // idle: no row of this warp is one
-            const int tok = real ? (x.qt * kRows + r) / A.group : 0;
+            const int tok = real ? (x.g0 + r) / A.group : 0;
             int klo, khi;  // keys that this row sees
             visible(s, window, tok, tok, klo, khi);
             if (!real) klo = khi = 0;
             // and those that every row of this tile sees: no mask for key tiles inside them
-            int alo, ahi;
-            {
-                const int r0 = x.qt * kRows + x.row0(i), r1 = min(r0 + 127, x.qt * kRows + x.rows - 1);
-                ahi = min(s.keys, s.base + r0 / A.group + 1);
-                alo = window > 0 ? max(0, s.base + r1 / A.group - window + 1) : 0;
-            }
+            const int r0 = x.g0 + x.row0(i), r1 = min(r0 + 127, x.g0 + x.rows - 1);
+            const int ahi = min(s.keys, s.base + r0 / A.group + 1);
+            const int alo = window > 0 ? max(0, s.base + r1 / A.group - window + 1) : 0;
             m = -INFINITY;
             l = 0.0f;
             for (int j = 0; j < n; ++j) {
                 const int k0 = (x.t0 + (x.thin() ? i : 0) + j * step) * kTile;
                 wait(bar_s + 8 * i, ns++);
-                if (j == 0 && i == 1 && nx[1] > 0) wait(bar_x + 8, nx[1] - 1);  // engine 0 has read the last thin part's O_1
+                if (j == 0 && i == 1 && nx > 0) wait(bar_x + 8, nx - 1);  // engine 0 has read the last thin part's O_1
                 if (idle) {  // its lanes of P are whatever they are: rows do not mix
                     tc_fence_before();
                     mbar_arrive(bar_p + 8 * i);
@@ -1019,8 +999,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                 }
                 if (k0 < alo || k0 + kTile > ahi) {
                     // keys that the row does not see: -infinity, written back, so that the
-                    // few such tiles share the code below (a second copy of it cost every
-                    // small call 10 us of instruction fetches)
+                    // few such tiles share the code below
                     const int lo = klo - k0, hi = khi - k0;
 #pragma unroll 1
                     for (int k = 0; k < 128; k += 16) {
@@ -1034,20 +1013,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                     }
                     tmem_wait_st();
                 }
-                uint32_t v[128];
+                // Two passes over the scores, 64 columns at a time in loops that stay
+                // loops, not one pass over 128 registers: every SM fetches the step's
+                // instructions anew in every call.  (1 over 650: 22.4 us, and 23.3 all
+                // unrolled; 32 at a time 4096 over 16384 takes 5% longer.)
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int k = 0; k < 128; k += 64) {
+                    uint32_t v[64];
+                    tmem_ld32(ts + k, v);
+                    tmem_ld32(ts + k + 32, v + 32);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld32(ts + 32 * k, v + 32 * k);
-                tmem_wait_ld();
-                float top[4];
+                    for (int t = 0; t < 64; t += 8)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) top[k] = __uint_as_float(v[k]);
-#pragma unroll
-                for (int k = 4; k < 124; k += 8)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        top[t] = fmaxf(top[t], fmaxf(__uint_as_float(v[k + t]), __uint_as_float(v[k + 4 + t])));
-#pragma unroll
-                for (int t = 0; t < 4; ++t) top[t] = fmaxf(top[t], __uint_as_float(v[124 + t]));
+                        for (int e = 0; e < 4; ++e)
+                            top[e] = fmaxf(top[e], fmaxf(__uint_as_float(v[t + e]), __uint_as_float(v[t + e + 4])));
+                }
                 const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 if (j == 0) {
                     m = mt;
@@ -1069,10 +1051,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                 const float mc = m == -INFINITY ? 0.0f : -m * c;
                 const uint64_t mc2 = pair(mc, mc);
                 uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t w[16];
-                    weights(v + 32 * k, c2, mc2, w, sum);
+#pragma unroll 2
+                for (int k = 0; k < 4; ++k) {  // weights over scores already read
+                    uint32_t v[32], w[16];
+                    tmem_ld32(ts + 32 * k, v);
+                    tmem_wait_ld();
+                    weights(v, c2, mc2, w, sum);
                     tmem_st16(ts + 16 * k, w);
                     if (k >= 2) {  // the first 96 keys' weights, then the last 32
                         tmem_wait_st();
@@ -1086,11 +1070,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                 l += a + b;
             }
         }
-        if (tid == 0) A.part_item[blockIdx.x] = cut;
     }
     tc_fence_before();
     __syncthreads();
-    __syncwarp();
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
