@@ -19,46 +19,66 @@ from . import _lib
 
 GROUP, BLOCK_BYTES = 128, 64
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16, torch.float32: _lib.F32}
+_BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+_get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+# A single token's call lasts a few microseconds on the GPU, so the checks come
+# twice: one expression that holds for every valid call, and, where it does not,
+# the checks one by one, which say what is wrong.
 
 
 def _on(t, dtype, dim, name, device=None):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    """A `dim`-dimensional CUDA tensor of the type, on the device (an index) if one is given; its device's index."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{name} is on {t.device}" + (f", expected {device}" if device is not None else ""))
+    at = t.get_device()
+    if at < 0 or (device is not None and at != device):
+        raise ValueError(f"{name} is on {t.device}" + (f", expected cuda:{device}" if device is not None else ""))
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions")
-    return t.device
+    return at
 
 
-def _contiguous(t, name):
+def _dense(t, dtype, dim, name, device=None):
+    """The same, contiguous."""
+    at = _on(t, dtype, dim, name, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return at
 
 
-def _strides(t, name):
+def _strides(t, shape, name):
     """Token and head strides of [tokens, heads, dim]; those of a dimension of size one say nothing."""
-    n, h, d = t.shape
-    if d > 1 and t.stride(2) != 1:
+    n, h, d = shape
+    st, sh, sd = t.stride()
+    if sd != 1 and d > 1:
         raise ValueError(f"{name}: the values of a head must be contiguous")
-    sh = t.stride(1) if h > 1 else (d + 7) // 8 * 8
-    return (t.stride(0) if n > 1 else h * sh), sh
+    if h <= 1:
+        sh = (d + 7) // 8 * 8
+    return (st if n > 1 else h * sh), sh
 
 
 def _call(fn, device, *args):
-    """The library call on `device`'s current stream, with that device current."""
-    f = getattr(_lib.load(), fn)
-    if torch.cuda.current_device() == device.index:
-        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    """The library call on the device's current stream, with that device current."""
+    f = getattr(_lib._lib or _lib.load(), fn)
+    if _get_device() == device:
+        rc = f(*args, _get_stream(device))
     else:
         with torch.cuda.device(device):
-            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+            rc = f(*args, _get_stream(device))
     if rc:
         _lib.check(rc, fn)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _tables_on(k_tables, v_tables):
+    dev = k_tables.device.index
+    if v_tables.device.index != dev:
+        raise ValueError(f"v_tables are on {v_tables.device}, k_tables on {k_tables.device}")
+    return _get_device() if dev is None else dev
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -116,18 +136,18 @@ def rope_table(n_positions: int, rotary_dim: int, base: float = 10000.0, scaling
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     if dev.type != "cuda":
         raise ValueError("the table lives on a CUDA device")
-    table = torch.empty((int(n_positions), rotary_dim // 2, 2), dtype=torch.float32, device=dev)
+    table = torch.empty((int(n_positions), rotary_dim // 2, 2), dtype=_F32, device=dev)
     arr = (ctypes.c_double * len(freq))(*freq)
-    _call("ecco_rope_table", table.device, arr, len(freq), magnitude, int(n_positions), table.data_ptr())
+    _call("ecco_rope_table", table.get_device(), arr, len(freq), magnitude, int(n_positions), table.data_ptr())
     return table
 
 
 def _table(rope, device):
-    _on(rope, torch.float32, 3, "table", device)
-    if rope.shape[2] != 2:
+    _dense(rope, _F32, 3, "table", device)
+    n, half, two = rope.shape
+    if two != 2:
         raise ValueError("table must be [n_positions, rotary_dim / 2, 2]")
-    _contiguous(rope, "table")
-    return rope.shape[0], 2 * rope.shape[1]
+    return n, 2 * half
 
 
 def _flags(interleaved, inverse):
@@ -143,48 +163,63 @@ def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, interlea
     result.  `out` may be x."""
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
         raise TypeError("x must be a bf16, fp16 or fp32 tensor")
-    dev = _on(x, x.dtype, 3, "x")
-    n, rotary = _table(table, dev)
-    _on(positions, torch.int32, 1, "positions", dev)
-    _contiguous(positions, "positions")
-    if positions.shape[0] != x.shape[0]:
+    dev, shape = x.get_device(), x.shape
+    if not (isinstance(table, torch.Tensor) and isinstance(positions, torch.Tensor) and dev >= 0 and len(shape) == 3
+            and table.dtype is _F32 and positions.dtype is _I32 and table.get_device() == positions.get_device() == dev
+            and table.dim() == 3 and positions.dim() == 1 and table.is_contiguous() and positions.is_contiguous()):
+        _on(x, x.dtype, 3, "x")
+        _table(table, dev)
+        _dense(positions, _I32, 1, "positions", dev)
+    tokens, heads, dim = shape
+    n, half, two = table.shape
+    if two != 2:
+        raise ValueError("table must be [n_positions, rotary_dim / 2, 2]")
+    rotary = 2 * half
+    if positions.shape[0] != tokens:
         raise ValueError("positions must have an entry for each row of x")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
     else:
         _on(out, x.dtype, 3, "out", dev)
-        if out.shape != x.shape:
+        if out.shape != shape:
             raise ValueError("out must have x's shape")
-    tokens, heads, dim = x.shape
-    _call("ecco_rope", dev, x.data_ptr(), *_strides(x, "x"), out.data_ptr(), *_strides(out, "out"), _DTYPES[x.dtype],
+    _call("ecco_rope", dev, x.data_ptr(), *_strides(x, shape, "x"), out.data_ptr(), *_strides(out, shape, "out"), _DTYPES[x.dtype],
           tokens, heads, dim, table.data_ptr(), n, rotary, positions.data_ptr(), _flags(interleaved, inverse))
     return out
 
 
 # ------------------------------------------------------------------ the paged cache
 def _paged(k_pages, v_pages, page_table, kv_lens, cu_q, device):
-    _on(k_pages, torch.uint8, 4, "k_pages", device)
-    _on(v_pages, torch.uint8, 4, "v_pages", device)
-    _on(page_table, torch.int32, 2, "page_table", device)
-    _on(kv_lens, torch.int32, 1, "kv_lens", device)
-    if k_pages.shape != v_pages.shape or k_pages.shape[3] != BLOCK_BYTES:
+    if not (isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor)
+            and isinstance(page_table, torch.Tensor) and isinstance(kv_lens, torch.Tensor)
+            and k_pages.dtype is v_pages.dtype is _U8 and page_table.dtype is kv_lens.dtype is _I32
+            and k_pages.get_device() == v_pages.get_device() == page_table.get_device() == kv_lens.get_device() == device
+            and k_pages.dim() == 4 and page_table.dim() == 2 and kv_lens.dim() == 1
+            and k_pages.is_contiguous() and v_pages.is_contiguous() and kv_lens.is_contiguous()):
+        _dense(k_pages, _U8, 4, "k_pages", device)
+        _dense(v_pages, _U8, 4, "v_pages", device)
+        _on(page_table, _I32, 2, "page_table", device)
+        _dense(kv_lens, _I32, 1, "kv_lens", device)
+    shape = k_pages.shape
+    n_pages, heads, page_size, block = shape
+    if v_pages.shape != shape or block != BLOCK_BYTES:
         raise ValueError("k_pages / v_pages must be [n_pages, kv_heads, page_size, 64] of the same shape")
-    _contiguous(k_pages, "k_pages")
-    _contiguous(v_pages, "v_pages")
-    _contiguous(kv_lens, "kv_lens")
     batch, max_pages = page_table.shape
-    if max_pages > 1 and page_table.stride(1) != 1:
+    stride, one = page_table.stride()
+    if one != 1 and max_pages > 1:
         raise ValueError("the entries of a page_table row must be contiguous")
     if kv_lens.shape[0] != batch:
         raise ValueError("kv_lens must have an entry for each row of page_table")
+    cu = None
     if cu_q is not None:
-        _on(cu_q, torch.int32, 1, "cu_q", device)
-        _contiguous(cu_q, "cu_q")
+        if not (isinstance(cu_q, torch.Tensor) and cu_q.dtype is _I32 and cu_q.get_device() == device and cu_q.dim() == 1
+                and cu_q.is_contiguous()):
+            _dense(cu_q, _I32, 1, "cu_q", device)
         if cu_q.shape[0] != batch + 1:
             raise ValueError("cu_q must have one entry more than page_table has rows")
-    n_pages, heads, page_size, _ = k_pages.shape
-    return _lib.Paged(n_pages, page_size, heads, batch, max_pages, page_table.stride(0) if batch > 1 else max_pages,
-                      page_table.data_ptr(), kv_lens.data_ptr(), _ptr(cu_q))
+        cu = cu_q.data_ptr()
+    return _lib.Paged(n_pages, page_size, heads, batch, max_pages, stride if batch > 1 else max_pages,
+                      page_table.data_ptr(), kv_lens.data_ptr(), cu)
 
 
 def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_tables, v_tables,
@@ -196,24 +231,25 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     - cu_q[b]) + i of sequence b (kv_lens counts the new tokens).  With `rope`
     (a rope_table of at most 128 values) the keys are turned first, by their own
     positions or by `positions` (int32 [tokens])."""
-    dev = k_tables.device
-    _on(k, torch.bfloat16, 3, "k", dev)
-    _on(v, torch.bfloat16, 3, "v", dev)
+    dev = _tables_on(k_tables, v_tables)
+    _on(k, _BF16, 3, "k", dev)
+    _on(v, _BF16, 3, "v", dev)
     p = _paged(k_pages, v_pages, page_table, kv_lens, cu_q, dev)
-    if k.shape != v.shape or k.shape[1] != p.kv_heads or k.shape[2] != GROUP:
+    shape = k.shape
+    tokens, heads, dim = shape
+    if v.shape != shape or heads != p.kv_heads or dim != GROUP:
         raise ValueError("k and v must be [tokens, kv_heads, 128]")
     n, rotary = (0, 0) if rope is None else _table(rope, dev)
     if positions is not None:
-        _on(positions, torch.int32, 1, "positions", dev)
-        _contiguous(positions, "positions")
-        if positions.shape[0] != k.shape[0]:
+        _dense(positions, _I32, 1, "positions", dev)
+        if positions.shape[0] != tokens:
             raise ValueError("positions must have an entry for each row of k")
     if stats is not None:
-        _on(stats, torch.int64, 1, "stats", dev)
-        if stats.numel() < len(_lib.STATS_FIELDS) or not stats.is_contiguous():
+        _dense(stats, torch.int64, 1, "stats", dev)
+        if stats.numel() < len(_lib.STATS_FIELDS):
             raise ValueError("stats must be a buffer of new_stats")
-    _call("ecco_paged_append", dev, k_tables.handle, v_tables.handle, p, k.data_ptr(), *_strides(k, "k"), v.data_ptr(),
-          *_strides(v, "v"), k.shape[0], k_pages.data_ptr(), v_pages.data_ptr(), _ptr(rope), n, rotary,
+    _call("ecco_paged_append", dev, k_tables.handle, v_tables.handle, p, k.data_ptr(), *_strides(k, shape, "k"), v.data_ptr(),
+          *_strides(v, shape, "v"), tokens, k_pages.data_ptr(), v_pages.data_ptr(), _ptr(rope), n, rotary,
           _ptr(positions), _flags(interleaved, inverse), _ptr(stats))
 
 
@@ -235,59 +271,60 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     tokens and the keys of one sequence (by default all rows, and what a
     page_table row holds); they size the workspace
     (paged_attention_workspace_bytes), which may be passed to reuse it."""
-    dev = k_tables.device
-    _on(q, torch.bfloat16, 3, "q", dev)
+    dev = _tables_on(k_tables, v_tables)
+    _on(q, _BF16, 3, "q", dev)
     p = _paged(k_pages, v_pages, page_table, kv_lens, cu_q, dev)
-    tokens, heads, dim = q.shape
-    if dim != GROUP or heads % p.kv_heads:
+    shape = q.shape
+    tokens, heads, dim = shape
+    kv_heads = p.kv_heads
+    if dim != GROUP or heads % kv_heads:
         raise ValueError("q must be [tokens, kv_heads * group, 128]")
-    group = heads // p.kv_heads
+    group = heads // kv_heads
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=_BF16, device=q.device)
     else:
-        _on(out, torch.bfloat16, 3, "out", dev)
-        if out.shape != q.shape:
+        _on(out, _BF16, 3, "out", dev)
+        if out.shape != shape:
             raise ValueError("out must have q's shape")
     if lse is not None:
-        _on(lse, torch.float32, 2, "lse", dev)
-        _contiguous(lse, "lse")
+        _dense(lse, _F32, 2, "lse", dev)
         if lse.shape != (tokens, heads):
             raise ValueError("lse must be [tokens, kv_heads * group]")
     max_q = tokens if max_q is None else int(max_q)
     max_kv = p.max_pages * p.page_size if max_kv is None else int(max_kv)
     if workspace is None:
-        workspace = torch.empty(max(1, paged_attention_workspace_bytes(p.batch, p.kv_heads, group, max_q, max_kv)),
-                                dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(1, paged_attention_workspace_bytes(p.batch, kv_heads, group, max_q, max_kv)),
+                                dtype=_U8, device=q.device)
     else:
-        _on(workspace, torch.uint8, 1, "workspace", dev)
-        _contiguous(workspace, "workspace")
+        _dense(workspace, _U8, 1, "workspace", dev)
     _call("ecco_paged_attention", dev, k_tables.handle, v_tables.handle, p, k_pages.data_ptr(), v_pages.data_ptr(),
-          q.data_ptr(), *_strides(q, "q"), group, tokens, max_q, max_kv, int(window), float(scale), out.data_ptr(),
-          *_strides(out, "out"), _ptr(lse), workspace.data_ptr(), workspace.numel())
+          q.data_ptr(), *_strides(q, shape, "q"), group, tokens, max_q, max_kv, int(window), float(scale), out.data_ptr(),
+          *_strides(out, shape, "out"), _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out
 
 
 def _host_ids(ids, name):
-    t = torch.as_tensor(ids, dtype=torch.int32) if not isinstance(ids, torch.Tensor) else ids
-    if t.dtype != torch.int32 or t.device.type != "cpu" or t.dim() != 1:
+    t = torch.as_tensor(ids, dtype=_I32) if not isinstance(ids, torch.Tensor) else ids
+    if t.dtype is not _I32 or t.get_device() >= 0 or t.dim() != 1:
         raise TypeError(f"{name} must be a list or a one-dimensional int32 CPU tensor")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def copy_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, src, dst) -> None:
     """Copies page src[i] to page dst[i] of both pools.  src and dst are page
     numbers on the host (lists or int32 CPU tensors); no destination may appear
     twice or be a source."""
-    dev = _on(k_pages, torch.uint8, 4, "k_pages")
-    _on(v_pages, torch.uint8, 4, "v_pages", dev)
-    if k_pages.shape != v_pages.shape or k_pages.shape[3] != BLOCK_BYTES:
+    if not (isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor) and k_pages.dtype is v_pages.dtype is _U8
+            and (dev := k_pages.get_device()) == v_pages.get_device() >= 0 and k_pages.dim() == 4
+            and k_pages.is_contiguous() and v_pages.is_contiguous()):
+        dev = _dense(k_pages, _U8, 4, "k_pages")
+        _dense(v_pages, _U8, 4, "v_pages", dev)
+    n_pages, heads, page_size, block = k_pages.shape
+    if v_pages.shape != k_pages.shape or block != BLOCK_BYTES:
         raise ValueError("k_pages / v_pages must be [n_pages, kv_heads, page_size, 64] of the same shape")
-    _contiguous(k_pages, "k_pages")
-    _contiguous(v_pages, "v_pages")
     src, dst = _host_ids(src, "src"), _host_ids(dst, "dst")
     if src.numel() != dst.numel():
         raise ValueError("src and dst must be of the same length")
-    n_pages, heads, page_size, _ = k_pages.shape
     _call("ecco_copy_pages", dev, k_pages.data_ptr(), v_pages.data_ptr(), n_pages, heads * page_size * BLOCK_BYTES,
           src.data_ptr(), dst.data_ptr(), src.numel())
 
@@ -299,20 +336,20 @@ def compact_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torc
     [batch, dst_pages]), in their order, and returns the new lengths (int32
     [batch]).  The blocks move as they are: nothing is encoded again.  The
     destination pages may not be among the pages read."""
-    dev = _on(k_pages, torch.uint8, 4, "k_pages")
+    dev = _on(k_pages, _U8, 4, "k_pages")
     p = _paged(k_pages, v_pages, page_table, kv_lens, None, dev)
-    _on(keep, keep.dtype if isinstance(keep, torch.Tensor) and keep.dtype in (torch.bool, torch.uint8) else torch.bool,
+    _on(keep, keep.dtype if isinstance(keep, torch.Tensor) and keep.dtype in (torch.bool, _U8) else torch.bool,
         2, "keep", dev)
-    _contiguous(keep, "keep")
-    _on(dst_table, torch.int32, 2, "dst_table", dev)
+    if not keep.is_contiguous():
+        raise ValueError("keep must be contiguous")
+    _on(dst_table, _I32, 2, "dst_table", dev)
     if dst_table.shape[1] > 1 and dst_table.stride(1) != 1:
         raise ValueError("the entries of a dst_table row must be contiguous")
     if keep.shape[0] != p.batch or dst_table.shape[0] != p.batch:
         raise ValueError("keep and dst_table must have a row for each of page_table")
     if out_lens is None:
-        out_lens = torch.empty(p.batch, dtype=torch.int32, device=dev)
-    _on(out_lens, torch.int32, 1, "out_lens", dev)
-    _contiguous(out_lens, "out_lens")
+        out_lens = torch.empty(p.batch, dtype=_I32, device=keep.device)
+    _dense(out_lens, _I32, 1, "out_lens", dev)
     if out_lens.shape[0] != p.batch:
         raise ValueError("out_lens must have an entry for each row of page_table")
     _call("ecco_compact_pages", dev, p, k_pages.data_ptr(), v_pages.data_ptr(), keep.data_ptr(), keep.shape[1],
@@ -490,12 +527,12 @@ class PagedCache:
         self.layers, self.kv_heads, self.page_size = len(self.k_tables), int(kv_heads), int(page_size)
         self.book = PageAllocator(n_pages, page_size)
         shape = (self.layers, n_pages, kv_heads, page_size, BLOCK_BYTES)
-        self.k_pages = torch.empty(shape, dtype=torch.uint8, device=self.device)
-        self.v_pages = torch.empty(shape, dtype=torch.uint8, device=self.device)
+        self.k_pages = torch.empty(shape, dtype=_U8, device=self.device)
+        self.v_pages = torch.empty(shape, dtype=_U8, device=self.device)
         self._position: dict[int, int] = {}
 
     def _ints(self, v):
-        return torch.tensor(v, dtype=torch.int32).to(self.device)
+        return torch.tensor(v, dtype=_I32).to(self.device)
 
     def _table_of(self, lists):
         width = max((len(p) for p in lists), default=0)
