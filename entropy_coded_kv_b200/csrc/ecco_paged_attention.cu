@@ -169,7 +169,7 @@ __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.
 constexpr int kDecThreads = 896;
 constexpr size_t kDecLut = sizeof(((DevTables*)0)->lut), kDecCt = sizeof(((DevTables*)0)->Ct);
 constexpr size_t kDecSmem = kSmemAlign + kDecLut + kDecCt + (size_t)16 * kDecThreads * 4 +
-                            (size_t)(2 * ECCO_MAX_BATCH + 1) * sizeof(int);
+                            (size_t)(3 * ECCO_MAX_BATCH + 1) * sizeof(int);
 
 struct StageArgs {
     ecco_paged p;
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     uint32_t* s_w = reinterpret_cast<uint32_t*>(smem + kDecLut + kDecCt);
     int* s_cu = reinterpret_cast<int*>(s_w + 16 * kDecThreads);  // [batch + 1] tiles before sequence b
     int* s_first = s_cu + ECCO_MAX_BATCH + 1;                    // [batch] its first tile
+    int* s_keys = s_first + ECCO_MAX_BATCH;                      // [batch] its keys
     const int tid = threadIdx.x;
     uint32_t* ws = s_w + tid;
     const int half = gridDim.x / 2, kv = blockIdx.x >= half;
@@ -211,9 +212,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     }
     for (int b = tid; b < A.p.batch; b += kDecThreads) {
         int first, count;
-        seq_tiles(seq_of(A.p, A.w, b), A.w.window, first, count);
+        const Seq s = seq_of(A.p, A.w, b);
+        seq_tiles(s, A.w.window, first, count);
         s_cu[b] = count;
         s_first[b] = first;
+        s_keys[b] = s.keys;
     }
     __syncthreads();
     if (tid < 32) warp_prefix(s_cu, A.p.batch, tid);
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         const int lin = (int)(i >> 7), h = lin / tiles, tile = lin - h * tiles;
         const int b = find_seq(s_cu, A.p.batch, tile);
         const int t = (s_first[b] + tile - s_cu[b]) * kTile + (int)(i & (kTile - 1));
-        if (t >= paged_kv_len(A.p, b, A.w.max_kv)) return nullptr;
+        if (t >= s_keys[b]) return nullptr;
         const int64_t blk = paged_block(A.p, b, A.h0 + h, t);
         return blk < 0 ? nullptr : pool + blk * ECCO_BLOCK_BYTES;
     };
@@ -792,14 +795,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
         const uint32_t ring = smem_u32(smem + kOffRing), qs = smem_u32(smem);
         const uint32_t idesc = kIdescQK | (A.scale < 0.0f ? kNegateA : 0u);
         uint32_t at = 0, np = 0, nq = 0;  // ring tiles taken; weights and queries waited for, a bit an engine (the parity)
-        auto settle = [&]() { ok = __all_sync(0xffffffffu, ok); };
-        auto full = [&](uint32_t k) {  // ring tile k has landed
-            if (ok) ok = mbar_wait(bar_full + 8 * (k % kStages), (k / kStages) & 1, dead, A.flag);
-            settle();
-        };
+        // The lanes agree on `ok` once a part.  Until then a wait that gave up (the
+        // CTA's other waits then end at once) only spoils results that nobody
+        // writes; a vote at each wait cost every step 500 cycles.
+        auto wait = [&](uint32_t bar, uint32_t parity) { ok = mbar_wait(bar, parity & 1, dead, A.flag) && ok; };
+        auto full = [&](uint32_t k) { wait(bar_full + 8 * (k % kStages), k / kStages); };  // ring tile k has landed
         for (;;) {
             const Part x = take();
-            settle();
+            ok = __all_sync(0xffffffffu, ok);
             if (lane == 0) give_back();
             if (!x.rows || !ok) break;
             if (x.n == 0) continue;
@@ -808,7 +811,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
             uint32_t v = 0, k = 0;  // ring tiles in use
             // step e: O_i += P_i times its values, then S_i of its engine's next keys (from step -2 on: S alone)
 #pragma unroll 1
-            for (int e = -2; e < steps && ok; ++e) {
+            for (int e = -2; e < steps; ++e) {
                 const int i = e & 1;
                 const bool fresh = thin || i == 0, last = thin || i == 1;  // of the engines that share the tiles
                 const bool more = (thin ? e + 2 : (e >> 1) + 1) < x.n;
@@ -820,37 +823,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                     const uint64_t b = sw128_desc(ring + (v % kStages) * kTileBytes);
 #pragma unroll
                     for (int piece = 0; piece < 2; ++piece) {  // the weights of 96 keys, then of the last 32
-                        if (ok) ok = mbar_wait(bar_p + 16 * piece + 8 * i, (np >> i) & 1, dead, A.flag);
-                        settle();
+                        wait(bar_p + 16 * piece + 8 * i, np >> i);
                         tc_fence_after();
-                        if (ok) {
 #pragma unroll
-                            for (int t = 6 * piece; t < 6 + 2 * piece; ++t)
-                                mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, b + (uint64_t)(t * 2048 >> 4), (e > 1 || t > 0) ? 1u : 0u, leader);
-                        }
+                        for (int t = 6 * piece; t < 6 + 2 * piece; ++t)
+                            mma_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * t, b + (uint64_t)(t * 2048 >> 4), (e > 1 || t > 0) ? 1u : 0u, leader);
                     }
                     np ^= 1u << i;
-                    if (ok) {
-                        mma_commit(bar_o + 8 * i, leader);
-                        if (last) mma_commit(bar_empty + 8 * (v % kStages), leader);
-                    }
+                    mma_commit(bar_o + 8 * i, leader);
+                    if (last) mma_commit(bar_empty + 8 * (v % kStages), leader);
                 }
                 if (more) {
                     if (e < 0) {
-                        if (ok) ok = mbar_wait(bar_q + 8 * i, (nq >> i) & 1, dead, A.flag);
-                        settle();
+                        wait(bar_q + 8 * i, nq >> i);
                         nq ^= 1u << i;
                     }
-                    if (ok) {
-                        const uint64_t a = sw128_desc(qs + i * kTileBytes), b = sw128_desc(ring + (k % kStages) * kTileBytes);
+                    const uint64_t a = sw128_desc(qs + i * kTileBytes), b = sw128_desc(ring + (k % kStages) * kTileBytes);
 #pragma unroll
-                        for (int t = 0; t < 8; ++t) {
-                            const uint64_t o = (uint64_t)(((t >> 2) * (kTileBytes / 2) + (t & 3) * 32) >> 4);
-                            mma_ss(tmem + 128 * i, a + o, b + o, idesc, t > 0, leader);
-                        }
-                        mma_commit(bar_s + 8 * i, leader);
-                        if (last) mma_commit(bar_empty + 8 * (k % kStages), leader);
+                    for (int t = 0; t < 8; ++t) {
+                        const uint64_t o = (uint64_t)(((t >> 2) * (kTileBytes / 2) + (t & 3) * 32) >> 4);
+                        mma_ss(tmem + 128 * i, a + o, b + o, idesc, t > 0, leader);
                     }
+                    mma_commit(bar_s + 8 * i, leader);
+                    if (last) mma_commit(bar_empty + 8 * (k % kStages), leader);
                 }
             }
         }
