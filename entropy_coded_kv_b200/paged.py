@@ -20,6 +20,7 @@ from . import _lib
 GROUP, BLOCK_BYTES = 128, 64
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16, torch.float32: _lib.F32}
 _BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+_CONTIGUOUS = torch.contiguous_format
 _get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 # A single token's call lasts a few microseconds on the GPU, so the checks come
@@ -178,7 +179,7 @@ def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, interlea
     if positions.shape[0] != tokens:
         raise ValueError("positions must have an entry for each row of x")
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=_CONTIGUOUS)
     else:
         _on(out, x.dtype, 3, "out", dev)
         if out.shape != shape:
@@ -281,7 +282,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         raise ValueError("q must be [tokens, kv_heads * group, 128]")
     group = heads // kv_heads
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=q.device)
+        out = torch.empty_like(q, memory_format=_CONTIGUOUS)
     else:
         _on(out, _BF16, 3, "out", dev)
         if out.shape != shape:
@@ -348,7 +349,7 @@ def compact_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torc
     if keep.shape[0] != p.batch or dst_table.shape[0] != p.batch:
         raise ValueError("keep and dst_table must have a row for each of page_table")
     if out_lens is None:
-        out_lens = torch.empty(p.batch, dtype=_I32, device=keep.device)
+        out_lens = torch.empty_like(kv_lens)
     _dense(out_lens, _I32, 1, "out_lens", dev)
     if out_lens.shape[0] != p.batch:
         raise ValueError("out_lens must have an entry for each row of page_table")
