@@ -357,7 +357,8 @@ struct AttnArgs {
     // 2c + 1 (an item that goes on in the next share) of CTA c
     float* part_o;   // [slot][32][slot_rows] float4
     float* part_ml;  // [slot][2][slot_rows]: maximum (in units of log2), sum
-    int4* part_item; // [CTA]: sequence, head, row tile, last CTA of the item begun in this share and unfinished; head < 0: none
+    int4* part_item; // [CTA]: the item begun in this share and unfinished -- first token row of its sequence, head (< 0: there
+                     // is none), first row, last CTA that has a part of it + 2^16 times its rows
     int slot_rows;
     int* flag;
 };
@@ -692,7 +693,7 @@ __device__ void plan_parts(const AttnArgs& A, uint8_t* smem, uint32_t bar_part, 
             hand(make_int4(s.q0, s.base, s.keys, qt * kRows), make_int4(r.rows, r.t0 + skip, min(until, r.n) - skip, begins | ends << 1),
                  make_int4(tile, tile + A.hn * tiles, h, 0));
             if (begins && !ends)
-                cut = make_int4(b, h, qt, (int)(((item + (long long)units * cost) * shares - 1) / total));
+                cut = make_int4(s.q0, h, qt * kRows, (int)(((item + (long long)units * cost) * shares - 1) / total) | r.rows << 16);
             item += (long long)units * cost;
             skip = 0;
             ++qt;
@@ -1071,51 +1072,67 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// Joins the parts of the items that were cut: block (c, piece) the item that
-// CTA c began and left unfinished.  A thread joins 4 values of a row; a warp
-// has 8 rows by 4 such pieces, which is 128 bytes of every part's columns and
-// a whole 32-byte sector of every output row.
-constexpr int kJoinThreads = 256;
+// Joins the parts of the items that were cut, in the order of their CTAs: block
+// (c, piece) the item that CTA c began and left unfinished.  A thread joins 4
+// values of kJoinRows rows, their loads in flight together; a warp has 8 rows
+// by 4 such pieces at a time, which is 128 bytes of every part's columns and a
+// whole 32-byte sector of every output row.
+constexpr int kJoinThreads = 256, kJoinRows = 2;
 
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnArgs A)
 {
     after_previous();
     const int4 it = A.part_item[blockIdx.x];
     if (it.y < 0) return;
-    const Seq s = seq_of(A.p, A.w, it.x);
-    const int rows = min(kRows, s.q * A.group - it.z * kRows);
-    const int at = blockIdx.y * kJoinThreads + threadIdx.x;  // (8 rows, 8 groups of 4 pieces, 4 pieces, row)
-    const int r = (at >> 8) * 8 + (at & 7), c4 = (at >> 3) & 31;
-    if (r >= rows) return;
-    const int c0 = blockIdx.x, c1 = it.w;
+    const int rows = it.w >> 16, c0 = blockIdx.x, c1 = it.w & 0xffff;
+    const int r0 = blockIdx.y * 8 * kJoinRows + (threadIdx.x & 7), c4 = threadIdx.x >> 3;  // rows r0, r0 + 8, ..
     const int64_t step = 2 * (int64_t)A.slot_rows;  // from slot to slot of part_ml; part_o has 16 times as many float4
-    const float* ml = A.part_ml + (2 * (int64_t)c0 + 1) * step + r;  // slot 2 c0 + 1, then 2 c of the others
-    const float4* po = reinterpret_cast<const float4*>(A.part_o) + (2 * (int64_t)c0 + 1) * 16 * step + (int64_t)c4 * A.slot_rows + r;
-    float m = ml[0], l = ml[A.slot_rows];
-    float4 o = *po;
-    ml += step;
-    po += 16 * step;
-#pragma unroll 4
-    for (int c = c0 + 1; c <= c1; ++c, ml += 2 * step, po += 32 * step) {
-        const float mc = ml[0], lc = ml[A.slot_rows];
-        const float4 v = *po;
-        const float mn = fmaxf(m, mc), f = m == -INFINITY ? 0.0f : exp2f(m - mn), g = mc == -INFINITY ? 0.0f : exp2f(mc - mn);
-        m = mn;
-        l = l * f + lc * g;
-        o.x = o.x * f + v.x * g;
-        o.y = o.y * f + v.y * g;
-        o.z = o.z * f + v.z * g;
-        o.w = o.w * f + v.w * g;
+    const float* ml = A.part_ml + (2 * (int64_t)c0 + 1) * step + r0;  // slot 2 c0 + 1, then 2 c of the others
+    const float4* po = reinterpret_cast<const float4*>(A.part_o) + (2 * (int64_t)c0 + 1) * 16 * step + (int64_t)c4 * A.slot_rows + r0;
+    float m[kJoinRows], l[kJoinRows];
+    float4 o[kJoinRows];
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+        m[k] = -INFINITY;
+        l[k] = 0.0f;
+        o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int g = it.z * kRows + r, qh = (A.h0 + it.y) * A.group + g % A.group;
-    const int64_t row = (int64_t)s.q0 + g / A.group;
-    uint2 w;
-    w.x = pack_bf16x2(o.x * inv, o.y * inv);
-    w.y = pack_bf16x2(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(A.out + row * A.out_token + (int64_t)qh * A.out_head + 4 * c4) = w;
-    if (A.lse && c4 == 0)
-        A.lse[row * A.p.kv_heads * A.group + qh] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+#pragma unroll 2
+    for (int c = c0; c <= c1; ++c) {
+        float mc[kJoinRows], lc[kJoinRows];
+        float4 v[kJoinRows];
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k)
+            if (r0 + 8 * k < rows) {
+                mc[k] = ml[8 * k];
+                lc[k] = ml[A.slot_rows + 8 * k];
+                v[k] = po[8 * k];
+            }
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k)
+            if (r0 + 8 * k < rows) {
+                const float mn = fmaxf(m[k], mc[k]);
+                const float f = m[k] == -INFINITY ? 0.0f : exp2f(m[k] - mn), g = mc[k] == -INFINITY ? 0.0f : exp2f(mc[k] - mn);
+                m[k] = mn;
+                l[k] = l[k] * f + lc[k] * g;
+                o[k] = make_float4(o[k].x * f + v[k].x * g, o[k].y * f + v[k].y * g, o[k].z * f + v[k].z * g, o[k].w * f + v[k].w * g);
+            }
+        ml += c == c0 ? step : 2 * step;
+        po += c == c0 ? 16 * step : 32 * step;
+    }
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k)
+        if (r0 + 8 * k < rows) {
+            const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
+            const int g = it.z + r0 + 8 * k, tok = g / A.group, qh = (A.h0 + it.y) * A.group + g - tok * A.group;
+            const int64_t row = (int64_t)it.x + tok;
+            uint2 w;
+            w.x = pack_bf16x2(o[k].x * inv, o[k].y * inv);
+            w.y = pack_bf16x2(o[k].z * inv, o[k].w * inv);
+            *reinterpret_cast<uint2*>(A.out + row * A.out_token + (int64_t)qh * A.out_head + 4 * c4) = w;
+            if (A.lse && c4 == 0)
+                A.lse[row * A.p.kv_heads * A.group + qh] = l[k] == 0.0f ? -INFINITY : (m[k] + log2f(l[k])) * 0.69314718f;
+        }
 }
 
 // Heads of a round: as many as keep the scratch within kRoundBytes, at least one.
@@ -1193,7 +1210,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* workspace, cuda
                           a.scale, reinterpret_cast<float*>(ws + L.o), reinterpret_cast<float*>(ws + L.ml),
                           reinterpret_cast<int4*>(ws), L.slot_rows, timeout_flag()};
         if ((e = launch_after(paged_attention_kernel, dim3(ctas), kAttnThreads, kAttnSmem, s, at)) != cudaSuccess) return e;
-        const dim3 join(ctas, ((L.slot_rows + 7) / 8 * 256 + kJoinThreads - 1) / kJoinThreads);
+        const dim3 join(ctas, (L.slot_rows + 8 * kJoinRows - 1) / (8 * kJoinRows));
         if ((e = launch_after(paged_join_kernel, join, kJoinThreads, 0, s, at)) != cudaSuccess) return e;
     }
     return cudaSuccess;
