@@ -564,6 +564,13 @@ struct Part {
     __device__ __forceinline__ int tiles(int i) const { return thin() ? (n + 1 - i) >> 1 : n; }
 };
 
+// a / b, not negative: in 32 bits where both fit (a 64-bit division costs 500
+// cycles, and the first part waits for four of them).
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The planning warp: works out the shares and hands this CTA's parts on.
 __device__ void plan_parts(const AttnArgs& A, uint8_t* smem, uint32_t bar_part, uint32_t bar_taken, volatile uint32_t* dead, int lane)
 {
@@ -638,7 +645,7 @@ __device__ void plan_parts(const AttnArgs& A, uint8_t* smem, uint32_t bar_part, 
         ++slot;
     };
     if (total > 0 && blockIdx.x < shares) {
-        const long long u0 = total * blockIdx.x / shares, stop = total * (blockIdx.x + 1) / shares;
+        const long long u0 = quotient(total * blockIdx.x, shares), stop = quotient(total * (blockIdx.x + 1), shares);
         int b = 0, top = batch - 1;  // the sequence of unit u0: the last that begins at or before it
         while (b < top) {
             const int mid = (b + top + 1) >> 1;
@@ -649,12 +656,9 @@ __device__ void plan_parts(const AttnArgs& A, uint8_t* smem, uint32_t bar_part, 
         }
         Seq s = P.seq(b);
         long long rem = u0 - P.units()[b];
-        const long long per_head = (P.units()[b + 1] - P.units()[b]) / A.hn;
-        int h = 0, qt = 0;
-        while (rem >= per_head) {
-            rem -= per_head;
-            ++h;
-        }
+        const long long per_head = quotient(P.units()[b + 1] - P.units()[b], A.hn);
+        int h = (int)quotient(rem, per_head), qt = 0;
+        rem -= h * per_head;
         const int n = (s.q * group + kRows - 1) / kRows;
         for (int q = 0; q < n; q += 32) {  // the item: 32 at a time
             Span r{0, 0, 0};
@@ -693,7 +697,7 @@ __device__ void plan_parts(const AttnArgs& A, uint8_t* smem, uint32_t bar_part, 
             hand(make_int4(s.q0, s.base, s.keys, qt * kRows), make_int4(r.rows, r.t0 + skip, min(until, r.n) - skip, begins | ends << 1),
                  make_int4(tile, tile + A.hn * tiles, h, 0));
             if (begins && !ends)
-                cut = make_int4(s.q0, h, qt * kRows, (int)(((item + (long long)units * cost) * shares - 1) / total) | r.rows << 16);
+                cut = make_int4(s.q0, h, qt * kRows, (int)quotient((item + (long long)units * cost) * shares - 1, total) | r.rows << 16);
             item += (long long)units * cost;
             skip = 0;
             ++qt;
@@ -719,24 +723,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int window = A.w.window;
 
-    if (tid == 0) {
-        for (int i = 0; i < 2 * kStages; ++i) mbar_init(bar_full + 8 * i, 1);
-        for (int i = 0; i < kParts; ++i) {
-            mbar_init(bar_part + 8 * i, 1);
-            mbar_init(bar_taken + 8 * i, 10);  // the softmax warps, products and copies
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar_q + 8 * i, 128);
-            mbar_init(bar_s + 8 * i, 1);
-            mbar_init(bar_p + 8 * i, 128);
-            mbar_init(bar_p + 16 + 8 * i, 128);
-            mbar_init(bar_o + 8 * i, 1);
-            mbar_init(bar_x + 8 * i, 128);
-        }
-        mbar_init(bar_end, 1);
-        *dead = 0u;
+    if (tid < kBars) {  // arrivals: softmax rows, the softmax warps with products and copies, or one
+        const uint32_t bar = bars + 8 * tid;
+        const bool rows = (bar >= bar_q && bar < bar_s) || (bar >= bar_p && bar < bar_o) || (bar >= bar_x && bar < bar_end);
+        mbar_init(bar, rows ? 128 : bar >= bar_taken && bar < bar_q ? 10 : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (tid == 0) *dead = 0u;
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "r"(512u)
                      : "memory");
