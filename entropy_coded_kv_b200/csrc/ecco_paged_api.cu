@@ -3,7 +3,6 @@
 // can see is checked here, and nothing is enqueued on an error.
 #include <algorithm>
 #include <cmath>
-#include <new>
 #include <vector>
 
 #include "ecco_paged.cuh"
@@ -110,7 +109,7 @@ extern "C" int ecco_paged_append(const ecco_tables* kt, const ecco_tables* vt, e
         (rc = check_strides(tokens, p.kv_heads, v_token, v_head, 8)))
         return rc;
     if (tokens == 0 || p.batch == 0 || p.n_pages == 0 || p.max_pages == 0) return ECCO_OK;
-    if (!k || !v || !k_pages || !v_pages) return ECCO_ERR_ARG;
+    if (!k || !v || !k_pages || !v_pages || k_pages == v_pages) return ECCO_ERR_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(rope, 16) ||
         !aligned(positions, 4) || !aligned(stats, 8))
         return ECCO_ERR_ALIGN;
@@ -181,7 +180,7 @@ extern "C" int ecco_copy_pages(uint8_t* k, uint8_t* v, int64_t n_pages, int64_t 
         }
         for (int64_t i = 0; i < n; ++i)
             if (written[src[i]]) return ECCO_ERR_ARG;
-    } catch (const std::bad_alloc&) {
+    } catch (...) {  // no memory for the marks: nothing may leave a C entry
         return ECCO_ERR_ARG;
     }
     return status(launch_copy_pages(k, v, page_bytes, src, dst, n, (cudaStream_t)stream));

@@ -52,7 +52,7 @@ def _strides(t, shape, name):
     """Token and head strides of [tokens, heads, dim]; those of a dimension of size one say nothing."""
     n, h, d = shape
     st, sh, sd = t.stride()
-    if sd != 1 and d > 1:
+    if sd != 1 and d > 1 and n and h:
         raise ValueError(f"{name}: the values of a head must be contiguous")
     if h <= 1:
         sh = (d + 7) // 8 * 8
@@ -207,7 +207,7 @@ def _paged(k_pages, v_pages, page_table, kv_lens, cu_q, device):
         raise ValueError("k_pages / v_pages must be [n_pages, kv_heads, page_size, 64] of the same shape")
     batch, max_pages = page_table.shape
     stride, one = page_table.stride()
-    if one != 1 and max_pages > 1:
+    if one != 1 and max_pages > 1 and batch:
         raise ValueError("the entries of a page_table row must be contiguous")
     if kv_lens.shape[0] != batch:
         raise ValueError("kv_lens must have an entry for each row of page_table")
@@ -344,7 +344,7 @@ def compact_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torc
     if not keep.is_contiguous():
         raise ValueError("keep must be contiguous")
     _on(dst_table, _I32, 2, "dst_table", dev)
-    if dst_table.shape[1] > 1 and dst_table.stride(1) != 1:
+    if dst_table.shape[1] > 1 and dst_table.stride(1) != 1 and p.batch:
         raise ValueError("the entries of a dst_table row must be contiguous")
     if keep.shape[0] != p.batch or dst_table.shape[0] != p.batch:
         raise ValueError("keep and dst_table must have a row for each of page_table")

@@ -355,8 +355,8 @@ int ecco_rope(const void* x, int64_t x_token_stride, int64_t x_head_stride, void
  * the row's pages, and entries that name no page are skipped.
  *   k, v        [tokens][kv_heads][128] bf16, strides in elements (multiples of
  *               8), the 128 values contiguous, 16-byte aligned;
- *   k_pages, v_pages  the pools, 16-byte aligned.  No page may appear twice
- *               among the pages that the call writes to;
+ *   k_pages, v_pages  the pools (two of them), 16-byte aligned.  No page may
+ *               appear twice among the pages that the call writes to;
  *   rotary_dim  as in ecco_rope with dim 128; ignored without a rope_table;
  *   dev_stats   may be NULL. */
 int ecco_paged_append(const ecco_tables* k_tables, const ecco_tables* v_tables, ecco_paged paged,
@@ -378,7 +378,8 @@ int ecco_paged_append(const ecco_tables* k_tables, const ecco_tables* v_tables, 
  * as they were.  Scores, softmax statistics and sums are fp32; the weights p_s
  * enter the second product as bf16, and the output is rounded to bf16.
  *   q, out      [tokens][kv_heads * group][128] bf16, token and head strides in
- *               elements (multiples of 8), 16-byte aligned;
+ *               elements (multiples of 8), 16-byte aligned; out may be q itself
+ *               (same strides), otherwise they may not overlap;
  *   lse         [tokens][kv_heads * group] fp32 contiguous, or NULL;
  *   max_q, max_kv  bounds of the new tokens and of the keys of a sequence;
  *               what lies past them (the last new tokens, the last keys) is
@@ -387,8 +388,11 @@ int ecco_paged_append(const ecco_tables* k_tables, const ecco_tables* v_tables, 
  *   workspace   caller-owned device scratch, 16-byte aligned, of
  *               ecco_paged_attention_workspace_bytes(...) bytes; no initial
  *               contents are needed.  Two calls that share it must be ordered.
+ * A sequence may share pages with others, and the pools may be one.
  * The blocks are decoded into the workspace (the KV heads in rounds of at most
- * 1 GiB) and read from there by the tensor-core kernel. */
+ * 1 GiB, or one head) and read from there by the tensor-core kernel.  Sums run
+ * in an order that depends on the lengths and the device alone: the same call
+ * gives the same bits.  ECCO_ERR_TIMEOUT: see ecco_device_timeouts. */
 size_t ecco_paged_attention_workspace_bytes(int batch, int kv_heads, int group, int max_q, int max_kv);
 int ecco_paged_attention(const ecco_tables* k_tables, const ecco_tables* v_tables, ecco_paged paged,
                          const uint8_t* k_pages, const uint8_t* v_pages, const uint16_t* q_bf16,
