@@ -1002,11 +1002,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                 }
                 if (k0 < alo || k0 + kTile > ahi) {
                     // keys that the row does not see: -infinity, written back, so that the
-                    // few such tiles share the code below
+                    // few such tiles share the code below.  16 columns at a time: left
+                    // alone where every row sees them, not read where none does.
                     const int lo = klo - k0, hi = khi - k0;
 #pragma unroll 1
                     for (int k = 0; k < 128; k += 16) {
+                        if (__all_sync(0xffffffffu, lo <= k && k + 16 <= hi)) continue;
                         uint32_t o[16];
+                        if (__all_sync(0xffffffffu, k >= hi || k + 16 <= lo)) {
+#pragma unroll
+                            for (int t = 0; t < 16; ++t) o[t] = 0xff800000u;
+                            tmem_st16(ts + k, o);
+                            continue;
+                        }
                         tmem_ld16(ts + k, o);
                         tmem_wait_ld();
 #pragma unroll
