@@ -51,6 +51,8 @@ def _dense(t, dtype, dim, name, device=None):
 def _strides(t, shape, name):
     """Token and head strides of [tokens, heads, dim]; those of a dimension of size one say nothing."""
     n, h, d = shape
+    if t.is_contiguous():
+        return h * d, d
     st, sh, sd = t.stride()
     if sd != 1 and d > 1 and n and h:
         raise ValueError(f"{name}: the values of a head must be contiguous")
@@ -67,7 +69,7 @@ def _call(fn, device, *args):
     else:
         with torch.cuda.device(device):
             rc = f(*args, _get_stream(device))
-    if rc:
+    if rc:  # _lib.ECCO_OK is 0
         _lib.check(rc, fn)
 
 
@@ -151,8 +153,7 @@ def _table(rope, device):
     return n, 2 * half
 
 
-def _flags(interleaved, inverse):
-    return (_lib.ROPE_INTERLEAVED if interleaved else 0) | (_lib.ROPE_INVERSE if inverse else 0)
+_FLAGS = ((0, _lib.ROPE_INVERSE), (_lib.ROPE_INTERLEAVED, _lib.ROPE_INTERLEAVED | _lib.ROPE_INVERSE))
 
 
 def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, interleaved: bool = False,
@@ -185,7 +186,7 @@ def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, interlea
         if out.shape != shape:
             raise ValueError("out must have x's shape")
     _call("ecco_rope", dev, x.data_ptr(), *_strides(x, shape, "x"), out.data_ptr(), *_strides(out, shape, "out"), _DTYPES[x.dtype],
-          tokens, heads, dim, table.data_ptr(), n, rotary, positions.data_ptr(), _flags(interleaved, inverse))
+          tokens, heads, dim, table.data_ptr(), n, rotary, positions.data_ptr(), _FLAGS[bool(interleaved)][bool(inverse)])
     return out
 
 
@@ -251,7 +252,7 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
             raise ValueError("stats must be a buffer of new_stats")
     _call("ecco_paged_append", dev, k_tables.handle, v_tables.handle, p, k.data_ptr(), *_strides(k, shape, "k"), v.data_ptr(),
           *_strides(v, shape, "v"), tokens, k_pages.data_ptr(), v_pages.data_ptr(), _ptr(rope), n, rotary,
-          _ptr(positions), _flags(interleaved, inverse), _ptr(stats))
+          _ptr(positions), _FLAGS[bool(interleaved)][bool(inverse)], _ptr(stats))
 
 
 def paged_attention_workspace_bytes(batch: int, kv_heads: int, group: int, max_q: int, max_kv: int) -> int:
