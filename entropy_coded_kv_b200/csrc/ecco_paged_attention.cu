@@ -1,16 +1,17 @@
 // Attention of new tokens over a paged compressed cache.
 //
-// Three kernels a round of KV heads: the visible keys' and values' blocks are
+// Few rows over few keys take one kernel (paged_small_kernel), everything else
+// three a round of KV heads: the visible keys' and values' blocks are
 // decoded into a scratch of 128-token tiles (each once, whatever the number of
 // new tokens), the attention kernel reads the tiles, and the items that it cut
 // are joined.  On one B200, 32 query and 8 KV heads, whole calls replayed from
 // a graph (medians; the long ones under the 1 kW power cap):
-//   1 new over 650 keys            22 us  (decode 10, attention 9, join 3)
+//   1 new over 650 keys          13.8 us  (one kernel; 22 in three)
 //   8 x 1 new over up to 4096      72 us  (decode 47, attention 21, join 3)
 //   500 new over 131072          1.43 ms  (decode 0.22; 750 TFLOP/s)
 //   4096 new over 16384          0.96 ms  (1.0 PFLOP/s; 0.83 ms at full clock)
 // The single tokens are bound by the decoder's serial walk (ecco_decode.cu) and
-// by latencies of a chain of three kernels, the prompts by the exponentials and
+// by latencies, the prompts by the exponentials and
 // the hand-overs between softmax and tensor cores.
 #include <algorithm>
 
@@ -1150,6 +1151,348 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         }
 }
 
+// ------------------------------------------------------------ few rows over few keys
+// One kernel for calls whose (sequence, KV head, key tile) triples all fit the
+// GPU at once, with at most 32 rows an item: a CTA decodes one tile of keys and
+// values straight into its shared memory, both tables with it, and computes its
+// part of the item.  An item's CTAs are a cluster and join their parts through
+// its shared memory, where an item has at most 8 tiles and the clusters all run
+// at once; otherwise the joining kernel does it, a part at a time, so that from
+// some 20 tiles on the three kernels above are as fast.  One against three, us a
+// call, 8 KV heads: 1 new over 100 keys 12.2 and 23.5, over 650 13.8 and 22.3,
+// over 2300 (18 tiles, joined by the kernel) 21.0 and 26.8; 8 new over 2300 23.3
+// and 27.6; but 1 new over 18000 keys of one head 63.5 and 46.3.
+//
+// Rows are TMEM lanes 0-31; the four warps that reach them (0, 4, 8, 12) weigh
+// 32 keys each and write 32 columns of the output each.  The rest of Q's 128-row
+// tile is whatever lies behind it in shared memory: rows of a product do not mix.
+constexpr int kSmallThreads = 512, kSmallRows = 32;
+constexpr size_t kSmallK = (size_t)kSmallRows * kG * 2, kSmallV = kSmallK + kTileBytes, kSmallLut = kSmallV + kTileBytes;
+constexpr size_t kSmallCt = kSmallLut + 2 * kDecLut, kSmallWords = kSmallCt + 2 * kDecCt;
+constexpr size_t kSmallExch = kSmallWords + (size_t)16 * 256 * 4;  // [2][4][32] maxima and sums
+constexpr size_t kSmallMl = kSmallExch + 2 * 4 * 32 * sizeof(float);  // [2][32] the tile's
+constexpr size_t kSmallBars = kSmallMl + 2 * 32 * sizeof(float);
+constexpr int kSmallCluster = 8, kSmallTiles = 20;
+constexpr size_t kSmallSmem = 1024 + kSmallBars + 32;
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// What lies at this CTA's shared address `at` in CTA `rank` of the cluster.
+__device__ __forceinline__ float ld_cluster(uint32_t at, uint32_t rank)
+{
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+        "ld.shared::cluster.f32 %0, [a];\n\t}"
+        : "=f"(v)
+        : "r"(at), "r"(rank)
+        : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t at, uint32_t rank)
+{
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(at), "r"(rank)
+        : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(kSmallThreads, 1) paged_small_kernel(const __grid_constant__ AttnArgs A,
+                                                                       const __grid_constant__ StageArgs D)
+{
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
+    const uint32_t bar_tables = smem_u32(smem + kSmallBars), bar_mma = bar_tables + 8;
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kSmallBars + 16);
+    volatile uint32_t* dead = s_tmem + 1;
+    float* s_max = reinterpret_cast<float*>(smem + kSmallExch);
+    float* s_sum = s_max + 4 * 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float4* s_o = reinterpret_cast<float4*>(smem + kSmallWords);  // [32 pieces of 4 values][32 rows], once the blocks are decoded
+    float* s_ml = reinterpret_cast<float*>(smem + kSmallMl);
+    uint32_t cluster;  // CTAs of the item, if they join their parts themselves; 1: a whole item, or left to the joining kernel
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cluster));
+    const int tile = blockIdx.x, h = blockIdx.y, b = blockIdx.z, cta = (b * gridDim.y + h) * gridDim.x + tile;
+    launch_dependents();
+    if (tid == 0) {
+        mbar_init(bar_tables, 1);
+        mbar_init(bar_mma, 1);
+        *dead = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        mbar_expect(bar_tables, (uint32_t)(2 * (kDecLut + kDecCt)));
+        for (int kv = 0; kv < 2; ++kv) {
+            bulk_copy(smem_u32(smem + kSmallLut + kv * kDecLut), &D.tb[kv]->lut[0][0], (uint32_t)kDecLut, bar_tables);
+            bulk_copy(smem_u32(smem + kSmallCt + kv * kDecCt), &D.tb[kv]->Ct[0][0], (uint32_t)kDecCt, bar_tables);
+        }
+    }
+    if (warp == 15) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)), "r"(256u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    const Seq s = seq_of(A.p, A.w, b);
+    const int window = A.w.window, rows = s.q * A.group;
+    int first, count;
+    seq_tiles(s, window, first, count);
+    const bool live = tile < count, none = count == 0 && tile == 0 && rows > 0;  // none: rows that see no key
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    bool ok = true;  // of a thread, then of the CTA, then of a warp
+
+    if (live) {
+        if (warp < 8) {  // ---- decode: thread = a row of the key tile, then of the value tile
+            const int kv = tid >> 7, row = tid & 127, t = (first + tile) * kTile + row;
+            uint4 q0 = make_uint4(0u, 0u, 0u, 0u), q1 = q0, q2 = q0, q3 = q0;
+            const int64_t blk = t < s.keys ? paged_block(A.p, b, h, t) : -1;
+            if (blk >= 0) {
+                const uint8_t* src = D.pages[kv] + blk * ECCO_BLOCK_BYTES;
+                q0 = ldg_nc_v4(src);
+                q1 = ldg_nc_v4(src + 16);
+                q2 = ldg_nc_v4(src + 32);
+                q3 = ldg_nc_v4(src + 48);
+            }
+            uint32_t* ws = reinterpret_cast<uint32_t*>(smem + kSmallWords) + tid;
+            const uint32_t code = q0.x & 0xffu;
+            const bool null = scale_code_is_null(code);
+            stage_words(ws, 256, q0, q1, q2, q3);
+            const float sc = __fmul_rn(D.tb[kv]->S_t, e4m3_to_f32(code));
+            ok = mbar_wait(bar_tables, 0u, dead, A.flag);
+            ok = __all_sync(0xffffffffu, ok);
+            const uint32_t lkey = lut_key(smem + kSmallLut + kv * kDecLut, (q0.x >> 8) & 255u);
+            ValuePlanes vp = make_planes(sc, reinterpret_cast<const float*>(smem + kSmallCt + kv * kDecCt), (int)((q0.x >> 8) & 63u));
+            if (null) {  // 128 times +0, whatever the stream says
+#pragma unroll
+                for (int k = 0; k < 4; ++k) vp.lo[k] = vp.hi[k] = 0u;
+            }
+            Stream st{q0.x, q0.y, kHdrBits, 2, kPayloadBits};
+            uint8_t* dst = smem + (kv ? kSmallV : kSmallK) + row * 128;
+            const uint32_t x = (uint32_t)row & 7u;
+            const auto put = [&](uint32_t c, const uint32_t (&a)[4]) {
+                *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTileBytes / 2) + (((c & 7u) ^ x) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
+            };
+            // Two warps a scheduler: the walk's latency is what counts.  The next word
+            // is there before it is needed, and the values of a chunk are worked out between
+            // the lookups of the next one.
+            uint32_t c = 0, a[4], nib = 0;
+            for (; ok && c < kG / 8; ++c) {
+                if (__any_sync(0xffffffffu, st.room < 64)) break;
+                const uint32_t last = nib;
+                int used = 0;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t next = st.widx < 16 ? ws[st.widx * 256] : 0u;
+                    uint32_t cur = __funnelshift_r(st.lo, st.hi, st.b);
+                    int u = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t e;
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(lkey ^ (cur & 0xffu)));
+                        const uint32_t len = e >> 4;
+                        nib = __funnelshift_r(nib, e, 4);
+                        cur >>= len;
+                        u += (int)len;
+                    }
+                    st.b += u;
+                    used += u;
+                    if (st.b >= 32) {
+                        st.lo = st.hi;
+                        st.hi = next;
+                        st.b -= 32;
+                        ++st.widx;
+                    }
+                    if (half == 0) {
+                        planes_to_bf16<0>(vp, last, last << 4, a[0], a[1]);
+                        planes_to_bf16<1>(vp, last, last << 4, a[2], a[3]);
+                        if (c > 0) put(c - 1, a);
+                    }
+                }
+                st.room -= used;
+            }
+            if (c > 0) {
+                planes_to_bf16<0>(vp, nib, nib << 4, a[0], a[1]);
+                planes_to_bf16<1>(vp, nib, nib << 4, a[2], a[3]);
+                put(c - 1, a);
+            }
+#pragma unroll 1
+            for (; ok && c < kG / 8; ++c) {  // near the end of the block
+                chunk_values(st, lkey, ws, 256, vp, a);
+                put(c, a);
+            }
+            if (ok && !null && st.room >= 0) {  // unclipped: outlier records follow the codewords
+                const int n = min(kMaxRec, st.room / kRecBits), at0 = kBlockBits - st.room;
+                for (int k = 0; k < n; ++k) {
+                    const uint32_t rec = read_record(ws, 256, at0 + k * kRecBits), e = rec & 127u;
+                    const float o = q_over_127((int)(int8_t)(uint8_t)(rec >> 7));
+                    *reinterpret_cast<uint16_t*>(dst + (e >> 6) * (kTileBytes / 2) + ((((e >> 3) & 7u) ^ x) << 4) + (e & 7u) * 2) =
+                        (uint16_t)f32_to_bf16_bits(__fmul_rn(sc, o));
+                }
+            }
+        } else if (warp == 8 && lane < rows) {  // ---- queries: lane = row
+            const int tok = lane / A.group;
+            const uint16_t* src = A.q + (int64_t)(s.q0 + tok) * A.q_token + (int64_t)(h * A.group + lane - tok * A.group) * A.q_head;
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                *reinterpret_cast<uint4*>(smem + (k >> 3) * (kSmallRows * 128) + lane * 128 + (((k & 7) ^ (lane & 7)) << 4)) =
+                    *reinterpret_cast<const uint4*>(src + 8 * k);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    __syncthreads();
+    ok = *dead == 0u;
+
+    if (live && warp == 9) {  // ---- products
+        const uint32_t leader = elect_one(), idesc = kIdescQK | (A.scale < 0.0f ? kNegateA : 0u);
+        const uint64_t kd = sw128_desc(smem_u32(smem + kSmallK)), vd = sw128_desc(smem_u32(smem + kSmallV));
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            mma_ss(tmem, sw128_desc(smem_u32(smem) + (t >> 2) * (kSmallRows * 128) + (t & 3) * 32),
+                   kd + (uint64_t)(((t >> 2) * (kTileBytes / 2) + (t & 3) * 32) >> 4), idesc, t > 0, leader);
+        mma_commit(bar_mma, leader);
+        asm volatile("bar.sync 2, 160;" ::: "memory");  // the weights are there
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mma_ts(tmem + 128, tmem + 8 * t, vd + (uint64_t)(t * 2048 >> 4), t > 0, leader);
+        mma_commit(bar_mma, leader);
+        uint32_t zero = 0u;  // every product is done before the tensor memory is freed
+        mbar_wait(bar_mma, 1u, &zero, nullptr);
+    } else if (live && (warp & 3) == 0) {  // ---- softmax: lane = row, this warp's keys 32 part .. of the tile
+        const int part = warp >> 2, tok = min(lane, rows - 1) / A.group;
+        const float c = fmaxf(fabsf(A.scale) * 1.44269504f, 1e-30f);
+        auto wait = [&](uint32_t parity) {
+            if (ok) ok = mbar_wait(bar_mma, parity, dead, A.flag);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+        };
+        int klo, khi;
+        visible(s, window, tok, tok, klo, khi);
+        klo -= (first + tile) * kTile + 32 * part;
+        khi -= (first + tile) * kTile + 32 * part;
+        const uint32_t seen = (khi >= 32 ? ~0u : khi > 0 ? (1u << khi) - 1u : 0u) & (klo <= 0 ? ~0u : klo < 32 ? ~0u << klo : 0u);
+        uint32_t v[32], w[16];
+        wait(0u);
+        tmem_ld32(tmem + 32 * part, v);
+        tmem_wait_ld();
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            if (!(seen >> k & 1u)) v[k] = 0xff800000u;
+            m = fmaxf(m, __uint_as_float(v[k]));
+        }
+        s_max[part * 32 + lane] = m;
+        tc_fence_before();
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // every warp has its scores in registers
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m = fmaxf(m, s_max[k * 32 + lane]);
+        const float mc = m == -INFINITY ? 0.0f : -m * c;
+        uint64_t sum[2] = {0ull, 0ull};
+        weights(v, pair(c, c), pair(mc, mc), w, sum);
+        float a, e;
+        unpair(add2(sum[0], sum[1]), a, e);
+        s_sum[part * 32 + lane] = a + e;
+        tmem_st16(tmem + 16 * part, w);
+        tmem_wait_st();
+        tc_fence_before();
+        asm volatile("bar.arrive 2, 160;" ::: "memory");
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        const float l = (s_sum[lane] + s_sum[32 + lane]) + (s_sum[64 + lane] + s_sum[96 + lane]);
+        wait(1u);
+        tmem_ld32(tmem + 128 + 32 * part, v);
+        tmem_wait_ld();
+        if (cluster > 1) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                s_o[(8 * part + k) * 32 + lane] = make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                                              __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]));
+            if (part == 0) {
+                s_ml[lane] = m == -INFINITY ? -INFINITY : m * c;
+                s_ml[32 + lane] = l;
+            }
+        } else if (ok && lane < rows) {
+            const int qh = h * A.group + lane - tok * A.group;
+            const int64_t at = (int64_t)s.q0 + tok;
+            if (count == 1) {  // the whole item
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                uint4* out = reinterpret_cast<uint4*>(A.out + at * A.out_token + (int64_t)qh * A.out_head) + 4 * part;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(__uint_as_float(v[2 * k]) * inv, __uint_as_float(v[2 * k + 1]) * inv);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) out[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                if (A.lse && part == 0)
+                    A.lse[at * A.p.kv_heads * A.group + qh] = l == 0.0f ? -INFINITY : fmaf(m, c * 0.69314718f, logf(l));
+            } else {
+                const int64_t slot = 2 * (int64_t)cta + (tile == 0 ? 1 : 0);
+                uint4* o = reinterpret_cast<uint4*>(A.part_o) + (slot * 32 + 8 * part) * A.slot_rows + lane;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[(int64_t)k * A.slot_rows] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                if (part == 0) {
+                    A.part_ml[slot * 2 * A.slot_rows + lane] = m == -INFINITY ? -INFINITY : m * c;
+                    A.part_ml[(slot * 2 + 1) * A.slot_rows + lane] = l;
+                }
+            }
+        }
+        tc_fence_before();
+    } else if (none && tid < rows * 16) {  // the first rows * 16 threads of the CTA: 16 bytes each
+        const int r = tid >> 4, tok = r / A.group, qh = h * A.group + r - tok * A.group;
+        const int64_t at = (int64_t)s.q0 + tok;
+        reinterpret_cast<uint4*>(A.out + at * A.out_token + (int64_t)qh * A.out_head)[tid & 15] = make_uint4(0u, 0u, 0u, 0u);
+        if (A.lse && (tid & 15) == 0) A.lse[at * A.p.kv_heads * A.group + qh] = -INFINITY;
+    }
+    if (cluster > 1) {  // ---- join: a thread 4 values of a row, CTA i the i-th 16 rows
+        cluster_arrive();
+        cluster_wait();
+        const int i = tile * kSmallThreads + tid, r = i >> 5, c4 = i & 31;
+        if (ok && count > 0 && r < rows) {
+            const uint32_t at_ml = smem_u32(s_ml + r), at_o = smem_u32(s_o + c4 * 32 + r);
+            float mc[kSmallCluster], lc[kSmallCluster], m = -INFINITY, l = 0.0f;
+            float4 v[kSmallCluster], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kSmallCluster; ++k)
+                if (k < count) {
+                    mc[k] = ld_cluster(at_ml, k);
+                    lc[k] = ld_cluster(at_ml + 128, k);
+                    v[k] = ld_cluster4(at_o, k);
+                    m = fmaxf(m, mc[k]);
+                }
+#pragma unroll
+            for (int k = 0; k < kSmallCluster; ++k)
+                if (k < count) {
+                    const float f = m == -INFINITY ? 0.0f : ex2(mc[k] - m);
+                    l = fmaf(lc[k], f, l);
+                    o = make_float4(fmaf(v[k].x, f, o.x), fmaf(v[k].y, f, o.y), fmaf(v[k].z, f, o.z), fmaf(v[k].w, f, o.w));
+                }
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const int tok = r / A.group, qh = h * A.group + r - tok * A.group;
+            const int64_t at = (int64_t)s.q0 + tok;
+            uint2 w;
+            w.x = pack_bf16x2(o.x * inv, o.y * inv);
+            w.y = pack_bf16x2(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2*>(A.out + at * A.out_token + (int64_t)qh * A.out_head + 4 * c4) = w;
+            if (A.lse && c4 == 0)
+                A.lse[at * A.p.kv_heads * A.group + qh] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
+        }
+        cluster_arrive();
+        cluster_wait();  // the others have read this CTA's part
+    }
+    if (tid == 0) {
+        if (cluster == 1) A.part_item[cta] = live && tile == 0 && count > 1 ? make_int4(s.q0, h, 0, (cta + count - 1) | rows << 16) : make_int4(0, -1, 0, 0);
+        if (!live) mbar_wait(bar_tables, 0u, dead, A.flag);  // the copies have landed before the CTA ends
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 15) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256u) : "memory");
+}
+
 // Heads of a round: as many as keep the scratch within kRoundBytes, at least one.
 int round_heads(int batch, int kv_heads, int max_kv)
 {
@@ -1202,11 +1545,50 @@ static cudaError_t launch_after(void (*kernel)(AttnArgs), dim3 grid, int threads
     return cudaLaunchKernelEx(&c, kernel, a);
 }
 
+static cudaLaunchAttribute cluster_of(int size)
+{
+    cudaLaunchAttribute c{};
+    c.id = cudaLaunchAttributeClusterDimension;
+    c.val.clusterDim.x = (unsigned)size;
+    c.val.clusterDim.y = c.val.clusterDim.z = 1;
+    return c;
+}
+
+static cudaLaunchConfig_t small_launch(dim3 grid, cudaLaunchAttribute* cluster, cudaStream_t s)
+{
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(kSmallThreads);
+    c.dynamicSmemBytes = kSmallSmem;
+    c.stream = s;
+    c.attrs = cluster;
+    c.numAttrs = 1;
+    return c;
+}
+
+// Clusters of `size` CTAs of the small kernel that the current device runs at
+// once (a cluster stays inside one of its processor groups); 0 if it can't say.
+static int clusters_at_once(int size)
+{
+    static std::atomic<int> cached[kMaxDeviceBits][kSmallCluster + 1];  // + 1; 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const bool slot = dev >= 0 && dev < kMaxDeviceBits;
+    int n = slot ? cached[dev][size].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n - 1;
+    cudaLaunchAttribute item = cluster_of(size);
+    const cudaLaunchConfig_t c = small_launch(dim3(size), &item, nullptr);
+    if (cudaOccupancyMaxActiveClusters(&n, paged_small_kernel, &c) != cudaSuccess) n = 0;
+    if (slot) cached[dev][size].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* workspace, cudaStream_t s)
 {
-    static std::atomic<uint64_t> configured[2]{};
+    static std::atomic<uint64_t> configured[3]{};
     cudaError_t e = set_max_smem_once(configured[0], (const void*)paged_decode_kernel, kDecSmem);
     if (e == cudaSuccess) e = set_max_smem_once(configured[1], (const void*)paged_attention_kernel, kAttnSmem);
+    if (e == cudaSuccess) e = set_max_smem_once(configured[2], (const void*)paged_small_kernel, kSmallSmem);
     if (e != cudaSuccess) return e;
     const Layout L = layout(a.p.batch, a.p.kv_heads, a.group, a.max_q, a.max_kv);
     uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 1023) / 1024 * 1024);
@@ -1215,18 +1597,37 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* workspace, cuda
     const int ctas = std::min(device_sm_count(), kMaxCtas);
     const Bounds w{a.tokens, a.max_q, a.max_kv, a.window};
     const bool wide = ((reinterpret_cast<uintptr_t>(a.pages[0]) | reinterpret_cast<uintptr_t>(a.pages[1])) & 31u) == 0;
+    const auto stage = [&](int h0, int n) {
+        return StageArgs{a.p, w, {a.tb[0], a.tb[1]}, {a.pages[0], a.pages[1]}, scratch, h0, n, wide, timeout_flag()};
+    };
+    const auto attn = [&](int h0, int n) {
+        return AttnArgs{a.p, w, scratch, a.q, a.out, a.lse, a.q_token, a.q_head, a.out_token, a.out_head, a.group, h0, n,
+                        a.scale, reinterpret_cast<float*>(ws + L.o), reinterpret_cast<float*>(ws + L.ml),
+                        reinterpret_cast<int4*>(ws), L.slot_rows, timeout_flag()};
+    };
+    const auto join = [&](int n_ctas, const AttnArgs& at) {
+        return launch_after(paged_join_kernel, dim3(n_ctas, (L.slot_rows + 8 * kJoinRows - 1) / (8 * kJoinRows)), kJoinThreads, 0, s, at);
+    };
+    // key tiles that an item can see
+    int64_t seen = std::max(1, (a.max_kv + kTile - 1) / kTile);
+    if (a.window > 0) seen = std::min<int64_t>(seen, ((int64_t)a.window + a.max_q - 2) / kTile + 2);
+    const int64_t triples = seen * a.p.kv_heads * a.p.batch;
+    if (L.slot_rows <= kSmallRows && seen <= kSmallTiles && triples <= ctas) {
+        const AttnArgs at = attn(0, a.p.kv_heads);
+        const bool together = seen <= kSmallCluster && (seen == 1 || clusters_at_once((int)seen) >= triples / seen);
+        cudaLaunchAttribute item = cluster_of(together ? (int)seen : 1);
+        const cudaLaunchConfig_t c = small_launch(dim3((unsigned)seen, a.p.kv_heads, a.p.batch), &item, s);
+        if ((e = cudaLaunchKernelEx(&c, paged_small_kernel, at, stage(0, a.p.kv_heads))) != cudaSuccess) return e;
+        return together ? cudaSuccess : join((int)triples, at);
+    }
     for (int h0 = 0; h0 < a.p.kv_heads; h0 += hn) {
         const int n = std::min(hn, a.p.kv_heads - h0);
-        const StageArgs st{a.p, w, {a.tb[0], a.tb[1]}, {a.pages[0], a.pages[1]}, scratch, h0, n, wide, timeout_flag()};
         // (the first kernel of a round waits for all before it: the workspace is free)
-        paged_decode_kernel<<<std::max(2, device_sm_count() & ~1), kDecThreads, kDecSmem, s>>>(st);
+        paged_decode_kernel<<<std::max(2, device_sm_count() & ~1), kDecThreads, kDecSmem, s>>>(stage(h0, n));
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        const AttnArgs at{a.p, w, scratch, a.q, a.out, a.lse, a.q_token, a.q_head, a.out_token, a.out_head, a.group, h0, n,
-                          a.scale, reinterpret_cast<float*>(ws + L.o), reinterpret_cast<float*>(ws + L.ml),
-                          reinterpret_cast<int4*>(ws), L.slot_rows, timeout_flag()};
+        const AttnArgs at = attn(h0, n);
         if ((e = launch_after(paged_attention_kernel, dim3(ctas), kAttnThreads, kAttnSmem, s, at)) != cudaSuccess) return e;
-        const dim3 join(ctas, (L.slot_rows + 8 * kJoinRows - 1) / (8 * kJoinRows));
-        if ((e = launch_after(paged_join_kernel, join, kJoinThreads, 0, s, at)) != cudaSuccess) return e;
+        if ((e = join(ctas, at)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

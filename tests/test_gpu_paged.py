@@ -249,6 +249,10 @@ def check_attention(out, lse, ref):
 
 @pytest.mark.parametrize("new,lens,H,G,page,window,scale,ktn,vtn,kk,vk", ATTEND)
 def test_attention(new, lens, H, G, page, window, scale, ktn, vtn, kk, vk):
+    one_attention(new, lens, H, G, page, window, scale, ktn, vtn, kk, vk)
+
+
+def one_attention(new, lens, H, G, page, window, scale, ktn, vtn, kk, vk, **bounds):
     kt, vt = table_set(ktn), table_set(vtn)
     n_pages = sum(-(-n // page) for n in lens) + 1
     table, kvl, cu = meta(lens, new, page, n_pages, seed=len(lens) + page)
@@ -256,9 +260,84 @@ def test_attention(new, lens, H, G, page, window, scale, ktn, vtn, kk, vk):
     pad = 2
     T = sum(new) + 2 * pad
     q = torch.randn(T, H * G, 128, generator=torch.Generator().manual_seed(T)).to(torch.bfloat16).to(DEV)
-    out, lse = run_attention(kb, vb, kt, vt, q, table, kvl, cu + pad, scale, window=window)
+    out, lse = run_attention(kb, vb, kt, vt, q, table, kvl, cu + pad, scale, window=window, **bounds)
     ref = attend(f64(bits(q)), pool_decode(kt, kb), pool_decode(vt, vb), table, kvl, cu + pad, scale, window)
     check_attention(out, lse, ref)
+
+
+@pytest.mark.parametrize("new,lens,H,G,page,window,scale,ktn,vtn,kk,vk", ATTEND)
+def test_attention_with_a_wide_bound(new, lens, H, G, page, window, scale, ktn, vtn, kk, vk):
+    """max_kv far above every length chooses the kernels, not the result."""
+    one_attention(new, lens, H, G, page, window, scale, ktn, vtn, kk, vk, max_kv=1 << 14)
+
+
+FEW = [
+    # new, lens, H, G, page, window, scale: at most 32 rows an item over few tiles
+    ([1], [128], 8, 4, 16, 0, 0.0884),
+    ([1], [129], 8, 4, 16, 0, 0.0884),
+    ([1], [650], 8, 4, 16, 0, 0.0884),
+    ([1, 1], [1000, 90], 8, 4, 64, 0, 0.0884),
+    ([1], [1100], 3, 5, 24, 0, 0.0884),
+    ([1, 2], [2500, 300], 2, 4, 48, 0, 0.0884),
+    ([1] * 37, list(range(1, 112, 3)), 4, 1, 8, 0, 0.0884),
+    ([1, 2, 0, 3], [900, 513, 300, 2], 3, 4, 100, 0, -0.05),
+    ([8], [1100], 2, 4, 24, 200, 0.0884),
+    ([32], [33], 1, 1, 7, 0, 0.0884),
+    ([16, 5], [256, 5], 2, 2, 32, 3, 0.0884),
+    ([4, 2, 1], [1, 0, 300], 2, 4, 16, 0, 0.0884),     # rows that see nothing
+    ([4, 2], [1, 0], 2, 4, 16, 0, 0.0884),             # in a call of one tile
+    ([2], [700], 1, 16, 33, 1, 0.0884),
+    ([3], [300], 2, 7, 16, 0, 0.0),
+    ([6], [400], 1, 4, 128, 0, 1.0),
+]
+
+
+@pytest.mark.parametrize("new,lens,H,G,page,window,scale", FEW)
+@pytest.mark.parametrize("kk,vk,max_kv", [("kv", "kv", None), ("special", "special", None), ("kv", "kv", 1 << 14)])
+def test_attention_few_rows(new, lens, H, G, page, window, scale, kk, vk, max_kv):
+    one_attention(new, lens, H, G, page, window, scale, "learned_kv", "random1", kk, vk, max_q=max(new), max_kv=max_kv)
+
+
+def test_attention_few_rows_bounds_garbage_and_bad_pages():
+    kt, vt = table_set("learned_kv"), table_set("random1")
+    rng = np.random.default_rng(9)
+    H, G, page, n_pages = 2, 4, 24, 40
+    kb, vb = (rng.integers(0, 256, (n_pages, H, page, 64), dtype=np.uint8) for _ in range(2))
+    table = rng.permutation(n_pages)[:39].reshape(3, 13).astype(np.int32)
+    table[0, 2], table[1, 5], table[2, 0] = -1, n_pages, 2**31 - 1
+    lens, new = np.array([300, 1000, 130], np.int32), [8, 5, 1]
+    cu = np.cumsum([0] + new).astype(np.int32)
+    q = torch.randn(14, H * G, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
+    kd, vd = pool_decode(kt, kb), pool_decode(vt, vb)
+    for max_q, max_kv, window in ((8, 312, 0), (8, 131, 0), (7, 312, 140), (1, 1, 0), (8, 0, 0), (8, 2000, 130), (3, 128, 0)):
+        out, lse = run_attention(kb, vb, kt, vt, q, table, lens, cu, 1e-3, max_q=max_q, max_kv=max_kv, window=window)
+        check_attention(out, lse, attend(f64(bits(q)), kd, vd, table, lens, cu, 1e-3, window, max_q, max_kv))
+    for bad_lens, bad_cu in (([-5, 2**31 - 1, -2**31], cu), (lens, [0, 40, 60, 90]), (lens, [-7, 3, 2, 30])):
+        for window in (0, 100):
+            run_attention(kb, vb, kt, vt, q, table, bad_lens, bad_cu, 1e-3, max_q=8, window=window)
+            torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kv", [100, 900, 1300])
+def test_attention_few_rows_nan_query_and_strides(kv):
+    """A NaN or infinite query spoils its own row only; q and out inside wider arrays, and one array."""
+    kt = vt = table_set("learned_kv")
+    H, G, page, new = 2, 4, 16, [7]
+    table, kvl, cu = meta([kv], new, page, -(-kv // page) + 1, seed=1)
+    kb, vb = (torch.from_numpy(fill_pool(kt, -(-kv // page) + 1, H, page, "kv", n)).to(DEV) for n in (3, 4))
+    wide = torch.randn(7, 3, H * G, 136, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).to(DEV)
+    q = wide[:, 1, :, 8:]
+    rest = (kb, vb, ecco.Tables(kt), ecco.Tables(vt), i32(table), i32(kvl), i32(cu), 0.0884)
+    clean = ecco.paged_attention(q.contiguous(), *rest)
+    q[5, 3, 5], q[2, 0, 0] = float("nan"), float("inf")
+    home = torch.zeros(H * G, 7, 144, dtype=torch.bfloat16, device=DEV)
+    out = home.transpose(0, 1)[..., :128]
+    ecco.paged_attention(q, *rest, out=out)
+    assert out[5, 3].isnan().all()
+    same = torch.ones(7, H * G, dtype=torch.bool, device=DEV)
+    same[5, 3] = same[2, 0] = False
+    assert torch.equal(out[same], clean[same]) and (home[..., 128:] == 0).all()
+    assert ecco.paged_attention(q, *rest, out=q) is q and torch.equal(q[same], clean[same])
 
 
 def test_attention_bounds_garbage_and_bad_pages():
