@@ -1088,33 +1088,49 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
     if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// Joins the parts of the items that were cut, in the order of their CTAs: block
-// (c, piece) the item that CTA c began and left unfinished.  A thread joins 4
-// values of kJoinRows rows, their loads in flight together; a warp has 8 rows
-// by 4 such pieces at a time, which is 128 bytes of every part's columns and a
-// whole 32-byte sector of every output row.
-constexpr int kJoinThreads = 256, kJoinRows = 2;
+// Joins the parts of the items that were cut, in a fixed order: block (c, piece)
+// the item that CTA c began and left unfinished.  A thread joins 4 values of
+// kJoinRows rows over every kJoinGroups-th part, their loads in flight together;
+// a warp has 8 rows by 4 such pieces at a time, which is 128 bytes of every
+// part's columns and a whole 32-byte sector of every output row.
+// Many parts are a chain of loads, so four groups share them where there are
+// many (16 or 32 shares an item) or the blocks few.  Whole calls, us, in one
+// group and in four: 1 new over 131072 keys of one head 102 and 65, 64 new over
+// 60000 of one head 112 and 69, 16 new over 8000 of 8 heads 43.7 and 40.0; but
+// 32 new over 8000 45.8 and 46.7, 512 new over 4096 64.8 and 79.5: many large
+// blocks, and two or three parts an item.
+struct Joined {  // of one row: maximum, sum, 4 values
+    float m, l;
+    float4 o;
+    __device__ __forceinline__ void add(float mc, float lc, const float4& v)
+    {
+        const float mn = fmaxf(m, mc), f = m == -INFINITY ? 0.0f : exp2f(m - mn), g = mc == -INFINITY ? 0.0f : exp2f(mc - mn);
+        m = mn;
+        l = l * f + lc * g;
+        o = make_float4(o.x * f + v.x * g, o.y * f + v.y * g, o.z * f + v.z * g, o.w * f + v.w * g);
+    }
+};
 
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnArgs A)
+template <int kJoinRows, int kJoinGroups>
+__global__ void __launch_bounds__(256 * kJoinGroups) paged_join_kernel(const __grid_constant__ AttnArgs A)
 {
+    constexpr int kOthers = kJoinGroups > 1 ? kJoinGroups - 1 : 1;
+    __shared__ float4 s_o[kOthers][kJoinRows][kJoinGroups > 1 ? 256 : 1];
+    __shared__ float2 s_ml[kOthers][kJoinRows][kJoinGroups > 1 ? 256 : 1];
     after_previous();
     const int4 it = A.part_item[blockIdx.x];
-    if (it.y < 0) return;
-    const int rows = it.w >> 16, c0 = blockIdx.x, c1 = it.w & 0xffff;
-    const int r0 = blockIdx.y * 8 * kJoinRows + (threadIdx.x & 7), c4 = threadIdx.x >> 3;  // rows r0, r0 + 8, ..
+    const int rows = it.w >> 16, c0 = blockIdx.x, c1 = it.w & 0xffff, t = threadIdx.x & 255, group = threadIdx.x >> 8;
+    if (it.y < 0 || (int)blockIdx.y * 8 * kJoinRows >= rows) return;
+    const int r0 = blockIdx.y * 8 * kJoinRows + (t & 7), c4 = t >> 3;  // rows r0, r0 + 8, ..
     const int64_t step = 2 * (int64_t)A.slot_rows;  // from slot to slot of part_ml; part_o has 16 times as many float4
-    const float* ml = A.part_ml + (2 * (int64_t)c0 + 1) * step + r0;  // slot 2 c0 + 1, then 2 c of the others
-    const float4* po = reinterpret_cast<const float4*>(A.part_o) + (2 * (int64_t)c0 + 1) * 16 * step + (int64_t)c4 * A.slot_rows + r0;
-    float m[kJoinRows], l[kJoinRows];
-    float4 o[kJoinRows];
+    const int64_t slot = 2 * ((int64_t)c0 + group) + (group == 0 ? 1 : 0);  // 2 c0 + 1, then 2 c of the others
+    const float* ml = A.part_ml + slot * step + r0;
+    const float4* po = reinterpret_cast<const float4*>(A.part_o) + slot * 16 * step + (int64_t)c4 * A.slot_rows + r0;
+    Joined x[kJoinRows];
 #pragma unroll
-    for (int k = 0; k < kJoinRows; ++k) {
-        m[k] = -INFINITY;
-        l[k] = 0.0f;
-        o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    }
+    for (int k = 0; k < kJoinRows; ++k) x[k] = Joined{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
 #pragma unroll 2
-    for (int c = c0; c <= c1; ++c) {
+    for (int c = c0 + group; c <= c1; c += kJoinGroups) {
         float mc[kJoinRows], lc[kJoinRows];
         float4 v[kJoinRows];
 #pragma unroll
@@ -1126,28 +1142,34 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
             }
 #pragma unroll
         for (int k = 0; k < kJoinRows; ++k)
-            if (r0 + 8 * k < rows) {
-                const float mn = fmaxf(m[k], mc[k]);
-                const float f = m[k] == -INFINITY ? 0.0f : exp2f(m[k] - mn), g = mc[k] == -INFINITY ? 0.0f : exp2f(mc[k] - mn);
-                m[k] = mn;
-                l[k] = l[k] * f + lc[k] * g;
-                o[k] = make_float4(o[k].x * f + v[k].x * g, o[k].y * f + v[k].y * g, o[k].z * f + v[k].z * g, o[k].w * f + v[k].w * g);
+            if (r0 + 8 * k < rows) x[k].add(mc[k], lc[k], v[k]);
+        ml += (2 * kJoinGroups - (c == c0 ? 1 : 0)) * step;
+        po += (2 * kJoinGroups - (c == c0 ? 1 : 0)) * 16 * step;
+    }
+    if constexpr (kJoinGroups > 1) {
+        if (group > 0)
+#pragma unroll
+            for (int k = 0; k < kJoinRows; ++k) {
+                s_o[group - 1][k][t] = x[k].o;
+                s_ml[group - 1][k][t] = make_float2(x[k].m, x[k].l);
             }
-        ml += c == c0 ? step : 2 * step;
-        po += c == c0 ? 16 * step : 32 * step;
+        __syncthreads();
+        if (group > 0) return;
     }
 #pragma unroll
     for (int k = 0; k < kJoinRows; ++k)
         if (r0 + 8 * k < rows) {
-            const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
+            if constexpr (kJoinGroups > 1)
+                for (int g = 1; g < kJoinGroups && c0 + g <= c1; ++g) x[k].add(s_ml[g - 1][k][t].x, s_ml[g - 1][k][t].y, s_o[g - 1][k][t]);
+            const float inv = x[k].l == 0.0f ? 0.0f : 1.0f / x[k].l;
             const int g = it.z + r0 + 8 * k, tok = g / A.group, qh = (A.h0 + it.y) * A.group + g - tok * A.group;
             const int64_t row = (int64_t)it.x + tok;
             uint2 w;
-            w.x = pack_bf16x2(o[k].x * inv, o[k].y * inv);
-            w.y = pack_bf16x2(o[k].z * inv, o[k].w * inv);
+            w.x = pack_bf16x2(x[k].o.x * inv, x[k].o.y * inv);
+            w.y = pack_bf16x2(x[k].o.z * inv, x[k].o.w * inv);
             *reinterpret_cast<uint2*>(A.out + row * A.out_token + (int64_t)qh * A.out_head + 4 * c4) = w;
             if (A.lse && c4 == 0)
-                A.lse[row * A.p.kv_heads * A.group + qh] = l[k] == 0.0f ? -INFINITY : (m[k] + log2f(l[k])) * 0.69314718f;
+                A.lse[row * A.p.kv_heads * A.group + qh] = x[k].l == 0.0f ? -INFINITY : (x[k].m + log2f(x[k].l)) * 0.69314718f;
         }
 }
 
@@ -1156,12 +1178,17 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 // GPU at once, with at most 32 rows an item: a CTA decodes one tile of keys and
 // values straight into its shared memory, both tables with it, and computes its
 // part of the item.  An item's CTAs are a cluster and join their parts through
-// its shared memory, where an item has at most 8 tiles and the clusters all run
-// at once; otherwise the joining kernel does it, a part at a time, so that from
-// some 20 tiles on the three kernels above are as fast.  One against three, us a
-// call, 8 KV heads: 1 new over 100 keys 12.2 and 23.5, over 650 13.8 and 22.3,
-// over 2300 (18 tiles, joined by the kernel) 21.0 and 26.8; 8 new over 2300 23.3
-// and 27.6; but 1 new over 18000 keys of one head 63.5 and 46.3.
+// its shared memory, where an item has at most 8 tiles and 8 rows and the
+// clusters all run at once (16 clusters of 8 did not: 29.5 us for 15.5);
+// otherwise the joining kernel does it.  By cluster and by the kernel, 4 query
+// heads over 650 keys: 1 new 13.7 and 15.0, 2 14.5 and 15.0, 4 15.9 and 15.1:
+// remote loads are slow, 60 cycles each.
+// One kernel, or one and the joining, against three with it, us a call: 8 KV
+// heads, 1 new over 100 keys 12.2 and 23.5, over 650 13.8 and 22.3, over 2300
+// (18 tiles) 16.6 and 22; 1 new over 7000 keys of 2 heads 20.5 and 27.8, over
+// 18000 of one 27.7 and 30.6, 8 new 29.0 and 32.2.
+// Of 11 us in the kernel the tables' landing takes 1.7, the walk 5, records,
+// scores and weights 2, the join 2.
 //
 // Rows are TMEM lanes 0-31; the four warps that reach them (0, 4, 8, 12) weigh
 // 32 keys each and write 32 columns of the output each.  The rest of Q's 128-row
@@ -1172,7 +1199,7 @@ constexpr size_t kSmallCt = kSmallLut + 2 * kDecLut, kSmallWords = kSmallCt + 2 
 constexpr size_t kSmallExch = kSmallWords + (size_t)16 * 256 * 4;  // [2][4][32] maxima and sums
 constexpr size_t kSmallMl = kSmallExch + 2 * 4 * 32 * sizeof(float);  // [2][32] the tile's
 constexpr size_t kSmallBars = kSmallMl + 2 * 32 * sizeof(float);
-constexpr int kSmallCluster = 8, kSmallTiles = 20;
+constexpr int kSmallCluster = 8, kSmallClusterRows = 8;
 constexpr size_t kSmallSmem = 1024 + kSmallBars + 32;
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
@@ -1448,11 +1475,11 @@ __global__ void __launch_bounds__(kSmallThreads, 1) paged_small_kernel(const __g
         reinterpret_cast<uint4*>(A.out + at * A.out_token + (int64_t)qh * A.out_head)[tid & 15] = make_uint4(0u, 0u, 0u, 0u);
         if (A.lse && (tid & 15) == 0) A.lse[at * A.p.kv_heads * A.group + qh] = -INFINITY;
     }
-    if (cluster > 1) {  // ---- join: a thread 4 values of a row, CTA i the i-th 16 rows
+    if (cluster > 1) {  // ---- join: the first CTA, a thread 4 values of one of its rows (at most kSmallThreads / 32)
         cluster_arrive();
         cluster_wait();
-        const int i = tile * kSmallThreads + tid, r = i >> 5, c4 = i & 31;
-        if (ok && count > 0 && r < rows) {
+        const int r = tid >> 5, c4 = tid & 31;
+        if (ok && tile == 0 && count > 0 && r < rows) {
             const uint32_t at_ml = smem_u32(s_ml + r), at_o = smem_u32(s_o + c4 * 32 + r);
             float mc[kSmallCluster], lc[kSmallCluster], m = -INFINITY, l = 0.0f;
             float4 v[kSmallCluster], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1606,15 +1633,19 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, void* workspace, cuda
                         reinterpret_cast<int4*>(ws), L.slot_rows, timeout_flag()};
     };
     const auto join = [&](int n_ctas, const AttnArgs& at) {
-        return launch_after(paged_join_kernel, dim3(n_ctas, (L.slot_rows + 8 * kJoinRows - 1) / (8 * kJoinRows)), kJoinThreads, 0, s, at);
+        const int64_t items = (int64_t)a.p.batch * at.hn * (((int64_t)a.max_q * a.group + kRows - 1) / kRows);
+        const bool few = L.slot_rows <= 32 || (L.slot_rows <= 64 && items * 16 <= ctas) || items * 32 <= ctas;
+        return few ? launch_after(paged_join_kernel<1, 4>, dim3(n_ctas, (L.slot_rows + 7) / 8), 1024, 0, s, at)
+                   : launch_after(paged_join_kernel<2, 1>, dim3(n_ctas, (L.slot_rows + 15) / 16), 256, 0, s, at);
     };
     // key tiles that an item can see
     int64_t seen = std::max(1, (a.max_kv + kTile - 1) / kTile);
     if (a.window > 0) seen = std::min<int64_t>(seen, ((int64_t)a.window + a.max_q - 2) / kTile + 2);
     const int64_t triples = seen * a.p.kv_heads * a.p.batch;
-    if (L.slot_rows <= kSmallRows && seen <= kSmallTiles && triples <= ctas) {
+    if (L.slot_rows <= kSmallRows && triples <= ctas) {
         const AttnArgs at = attn(0, a.p.kv_heads);
-        const bool together = seen <= kSmallCluster && (seen == 1 || clusters_at_once((int)seen) >= triples / seen);
+        const bool together = seen == 1 || (seen <= kSmallCluster && L.slot_rows <= kSmallClusterRows &&
+                                            clusters_at_once((int)seen) >= triples / seen);
         cudaLaunchAttribute item = cluster_of(together ? (int)seen : 1);
         const cudaLaunchConfig_t c = small_launch(dim3((unsigned)seen, a.p.kv_heads, a.p.batch), &item, s);
         if ((e = cudaLaunchKernelEx(&c, paged_small_kernel, at, stage(0, a.p.kv_heads))) != cudaSuccess) return e;

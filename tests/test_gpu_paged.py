@@ -289,6 +289,9 @@ FEW = [
     ([2], [700], 1, 16, 33, 1, 0.0884),
     ([3], [300], 2, 7, 16, 0, 0.0),
     ([6], [400], 1, 4, 128, 0, 1.0),
+    ([2, 1, 0, 2, 2], [0, 300, 500, 1, 129], 2, 3, 16, 0, 0.0884),
+    ([2, 1], [1000, 500], 3, 4, 48, 300, -0.05),
+    ([8, 8], [1024, 8], 1, 1, 32, 2, 0.0884),
 ]
 
 
@@ -309,7 +312,7 @@ def test_attention_few_rows_bounds_garbage_and_bad_pages():
     cu = np.cumsum([0] + new).astype(np.int32)
     q = torch.randn(14, H * G, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
     kd, vd = pool_decode(kt, kb), pool_decode(vt, vb)
-    for max_q, max_kv, window in ((8, 312, 0), (8, 131, 0), (7, 312, 140), (1, 1, 0), (8, 0, 0), (8, 2000, 130), (3, 128, 0)):
+    for max_q, max_kv, window in ((8, 312, 0), (8, 131, 0), (7, 312, 140), (1, 1, 0), (8, 0, 0), (8, 2000, 130), (3, 128, 0), (2, 312, 0), (2, 2000, 140)):
         out, lse = run_attention(kb, vb, kt, vt, q, table, lens, cu, 1e-3, max_q=max_q, max_kv=max_kv, window=window)
         check_attention(out, lse, attend(f64(bits(q)), kd, vd, table, lens, cu, 1e-3, window, max_q, max_kv))
     for bad_lens, bad_cu in (([-5, 2**31 - 1, -2**31], cu), (lens, [0, 40, 60, 90]), (lens, [-7, 3, 2, 30])):
@@ -318,24 +321,24 @@ def test_attention_few_rows_bounds_garbage_and_bad_pages():
             torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("kv", [100, 900, 1300])
-def test_attention_few_rows_nan_query_and_strides(kv):
+@pytest.mark.parametrize("kv,G", [(100, 4), (900, 4), (1300, 4), (900, 1)])
+def test_attention_few_rows_nan_query_and_strides(kv, G):
     """A NaN or infinite query spoils its own row only; q and out inside wider arrays, and one array."""
     kt = vt = table_set("learned_kv")
-    H, G, page, new = 2, 4, 16, [7]
+    H, page, new = 2, 16, [7]
     table, kvl, cu = meta([kv], new, page, -(-kv // page) + 1, seed=1)
     kb, vb = (torch.from_numpy(fill_pool(kt, -(-kv // page) + 1, H, page, "kv", n)).to(DEV) for n in (3, 4))
     wide = torch.randn(7, 3, H * G, 136, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).to(DEV)
     q = wide[:, 1, :, 8:]
     rest = (kb, vb, ecco.Tables(kt), ecco.Tables(vt), i32(table), i32(kvl), i32(cu), 0.0884)
     clean = ecco.paged_attention(q.contiguous(), *rest)
-    q[5, 3, 5], q[2, 0, 0] = float("nan"), float("inf")
+    q[5, 1, 5], q[2, 0, 0] = float("nan"), float("inf")
     home = torch.zeros(H * G, 7, 144, dtype=torch.bfloat16, device=DEV)
     out = home.transpose(0, 1)[..., :128]
     ecco.paged_attention(q, *rest, out=out)
-    assert out[5, 3].isnan().all()
+    assert out[5, 1].isnan().all()
     same = torch.ones(7, H * G, dtype=torch.bool, device=DEV)
-    same[5, 3] = same[2, 0] = False
+    same[5, 1] = same[2, 0] = False
     assert torch.equal(out[same], clean[same]) and (home[..., 128:] == 0).all()
     assert ecco.paged_attention(q, *rest, out=q) is q and torch.equal(q[same], clean[same])
 
