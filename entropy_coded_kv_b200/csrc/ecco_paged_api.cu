@@ -151,6 +151,7 @@ extern "C" int ecco_paged_attention(const ecco_tables* kt, const ecco_tables* vt
         (rc = check_strides(tokens, heads, out_token, out_head, 8)))
         return rc;
     if (rows_overlap(tokens, heads, out_token, out_head, kG)) return ECCO_ERR_ARG;
+    if (q == out && (q_token != out_token || q_head != out_head)) return ECCO_ERR_ARG;
     if (tokens == 0 || p.batch == 0 || max_q == 0) return ECCO_OK;
     if (!q || !out || !ws || (p.n_pages > 0 && (!k_pages || !v_pages))) return ECCO_ERR_ARG;
     if (ws_bytes < ecco_paged_attention_workspace_bytes(p.batch, p.kv_heads, group, max_q, max_kv)) return ECCO_ERR_ARG;
@@ -202,6 +203,9 @@ extern "C" int ecco_compact_pages(ecco_paged p, uint8_t* k_pages, uint8_t* v_pag
     if (p.n_pages > 0 && (!k_pages || !v_pages)) return ECCO_ERR_ARG;
     if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(dst_table, 4) || !aligned(new_lens, 4))
         return ECCO_ERR_ALIGN;
+    // the lengths are read by every CTA of a sequence and written by one of them
+    const uintptr_t out = reinterpret_cast<uintptr_t>(new_lens), in = reinterpret_cast<uintptr_t>(p.kv_lens), n = 4u * (uintptr_t)p.batch;
+    if (out < in + n && in < out + n) return ECCO_ERR_ARG;
     const CompactArgs a{p, {k_pages, v_pages}, keep, keep_stride, dst_table, dst_stride, dst_max_pages, new_lens};
     return status(launch_compact_pages(a, (cudaStream_t)stream));
 }

@@ -1605,7 +1605,10 @@ static int clusters_at_once(int size)
     if (n > 0) return n - 1;
     cudaLaunchAttribute item = cluster_of(size);
     const cudaLaunchConfig_t c = small_launch(dim3(size), &item, nullptr);
-    if (cudaOccupancyMaxActiveClusters(&n, paged_small_kernel, &c) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, paged_small_kernel, &c) != cudaSuccess) {
+        cudaGetLastError();  // not this call's
+        n = 0;
+    }
     if (slot) cached[dev][size].store(n + 1, std::memory_order_relaxed);
     return n;
 }

@@ -336,8 +336,9 @@ def compact_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torc
     """Moves the kept tokens of each sequence (keep: bool or uint8 [batch, at
     least the longest length]) to the front of the pages dst_table (int32
     [batch, dst_pages]), in their order, and returns the new lengths (int32
-    [batch]).  The blocks move as they are: nothing is encoded again.  The
-    destination pages may not be among the pages read."""
+    [batch]; `out_lens` may not be kv_lens).  The blocks move as they are:
+    nothing is encoded again.  The destination pages may not be among the pages
+    read."""
     dev = _on(k_pages, _U8, 4, "k_pages")
     p = _paged(k_pages, v_pages, page_table, kv_lens, None, dev)
     _on(keep, keep.dtype if isinstance(keep, torch.Tensor) and keep.dtype in (torch.bool, _U8) else torch.bool,
@@ -561,6 +562,8 @@ class PagedCache:
         """Pages for new[i] more tokens of each sequence (OutOfPages if there are
         too few, with nothing changed), and the batch's view for the layers'
         calls.  Pages that are shared and about to be written are copied."""
+        if len(seqs) > _lib.MAX_BATCH:
+            raise ValueError(f"at most {_lib.MAX_BATCH} sequences a step")
         copies = self.book.extend(seqs, new)
         if copies:
             n = self.book.n_pages
@@ -603,6 +606,8 @@ class PagedCache:
         and frees the pages that are left over.  Takes as many free pages as the
         sequences hold while it runs.  Blocks until the new lengths are known;
         returns them."""
+        if len(seqs) > _lib.MAX_BATCH:
+            raise ValueError(f"at most {_lib.MAX_BATCH} sequences a call")
         lens = [self.book.length(s) for s in seqs]
         if keep.dim() != 2 or keep.shape[0] != len(seqs) or keep.shape[1] < max(lens, default=0):
             raise ValueError("keep must be [len(seqs), at least the longest length]")

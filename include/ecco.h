@@ -420,7 +420,8 @@ int ecco_copy_pages(uint8_t* k_pages, uint8_t* v_pages, int64_t n_pages, int64_t
  *             bytes apart; only the first kv_lens[b] of a row are read, and
  *             none at or past keep_stride;
  *   dst_table [batch][dst_max_pages] int32, dst_stride entries apart; keep,
- *             dst_table and new_lens are device memory. */
+ *             dst_table and new_lens are device memory; new_lens may not
+ *             overlap kv_lens (ECCO_ERR_ARG). */
 int ecco_compact_pages(ecco_paged paged, uint8_t* k_pages, uint8_t* v_pages, const uint8_t* keep,
                        int64_t keep_stride, const int32_t* dst_table, int64_t dst_stride, int dst_max_pages,
                        int32_t* new_lens, void* stream);

@@ -521,14 +521,15 @@ def test_pools_past_32_bits():
             assert torch.equal(vp[third[b, t // page], :, t % page], vp[other[b, (2 * t + 1) // page], :, (2 * t + 1) % page])
 
 
-def test_attention_in_place_and_on_two_streams():
+@pytest.mark.parametrize("lens,new", [([700, 90], [100, 1]), ([700, 90], [1, 1]), ([1500, 90], [3, 1])])
+def test_attention_in_place_and_on_two_streams(lens, new):
     """out = q, and two calls at once on two streams with a workspace each."""
     kt = vt = table_set("learned_kv")
-    H, G, page, lens, new = 2, 4, 16, [700, 90], [100, 1]
-    table, kvl, cu = meta(lens, new, page, 60, seed=1)
-    kp, vp = (torch.from_numpy(fill_pool(kt, 60, H, page, "kv", s)).to(DEV) for s in (3, 4))
+    H, G, page = 2, 4, 16
+    table, kvl, cu = meta(lens, new, page, 110, seed=1)
+    kp, vp = (torch.from_numpy(fill_pool(kt, 110, H, page, "kv", s)).to(DEV) for s in (3, 4))
     kT, tb, kv, cq = ecco.Tables(kt), i32(table), i32(kvl), i32(cu)
-    qs = [torch.randn(101, H * G, 128, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    qs = [torch.randn(sum(new), H * G, 128, device=DEV).to(torch.bfloat16) for _ in range(2)]
     want = [ecco.paged_attention(q, kp, vp, kT, kT, tb, kv, cq, 0.0884) for q in qs]
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
@@ -697,7 +698,8 @@ def test_cache_from_prompt_to_fork_to_compaction():
     step([d], [1])
 
 
-def test_captured_step_replays_on_new_lengths_and_streams():
+@pytest.mark.parametrize("max_kv", [240, 1 << 14])
+def test_captured_step_replays_on_new_lengths_and_streams(max_kv):
     """Append and attention captured into a graph on a side stream; replays
     follow the page table and lengths written between them.  Two graphs share
     one workspace, replayed in order."""
@@ -708,14 +710,14 @@ def test_captured_step_replays_on_new_lengths_and_streams():
     table = np.random.default_rng(1).permutation(n_pages)[:30].reshape(2, 15).astype(np.int32)
     tb, lens, cu = i32(table), i32([10, 20]), i32([0, 1, 2])
     k, v, q = (torch.randn(B, n, 128, device=DEV).to(torch.bfloat16) for n in (H, H, H * G))
-    ws = torch.empty(ecco.paged_attention_workspace_bytes(B, H, G, 1, 240), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(ecco.paged_attention_workspace_bytes(B, H, G, 1, max_kv), dtype=torch.uint8, device=DEV)
     rt = ecco.rope_table(240, 128)
     outs = [torch.empty_like(q) for _ in range(2)]
     side, graphs = torch.cuda.Stream(), []
 
     def once(o):
         ecco.paged_append(k, v, kp, vp, kT, vT, tb, lens, cu, rope=rt)
-        ecco.paged_attention(q, kp, vp, kT, vT, tb, lens, cu, 0.0884, max_q=1, max_kv=240, out=o, workspace=ws)
+        ecco.paged_attention(q, kp, vp, kT, vT, tb, lens, cu, 0.0884, max_q=1, max_kv=max_kv, out=o, workspace=ws)
 
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -770,3 +772,21 @@ def test_refusals_of_the_binding():
         ecco.copy_pages(kp, kp.clone(), i32([0]), [1])
     with pytest.raises(ValueError):
         ecco.compact_pages(kp, kp.clone(), tb, lens, torch.ones(2, 9, dtype=torch.bool, device=DEV), tb)
+
+
+def test_refusals_of_one_array_twice_and_of_wide_steps():
+    t = ecco.Tables(table_set("learned_kv"))
+    kp = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, device=DEV)
+    tb, lens, cu = i32([[0, 1]]), i32([5]), i32([0, 8])
+    q = torch.zeros(8, 8, 128, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ecco.EccoError):  # q's rows, head by head
+        ecco.paged_attention(q, kp, kp, t, t, tb, lens, cu, 1.0, out=q.transpose(0, 1))
+    with pytest.raises(ecco.EccoError):
+        ecco.compact_pages(kp, kp.clone(), tb, lens, torch.ones(1, 32, dtype=torch.bool, device=DEV), i32([[2, 3]]), out_lens=lens)
+    cache = ecco.PagedCache(8, 16, 2, t, t)
+    seqs = [cache.add() for _ in range(_lib.MAX_BATCH + 1)]
+    with pytest.raises(ValueError):
+        cache.extend(seqs, [0] * len(seqs))
+    with pytest.raises(ValueError):
+        cache.compact(seqs, torch.ones(len(seqs), 1, dtype=torch.bool, device=DEV))
+    assert cache.extend(seqs[1:], [0] * _lib.MAX_BATCH).tokens == 0

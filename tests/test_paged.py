@@ -187,6 +187,10 @@ def test_compact_refusals(lib):
     assert compact(lib, p, pages=4104) == _lib.ECCO_ERR_ALIGN
     assert compact(lib, p, lens=4098) == _lib.ECCO_ERR_ALIGN
     assert compact(lib, paged(page_table=4097)) == _lib.ECCO_ERR_ALIGN
+    # lengths written where others are read
+    assert compact(lib, p) == _lib.ECCO_ERR_ARG
+    assert compact(lib, paged(batch=3, kv_lens=8192), lens=8200) == _lib.ECCO_ERR_ARG
+    assert compact(lib, paged(batch=3, kv_lens=8200), lens=8192) == _lib.ECCO_ERR_ARG
     assert compact(lib, paged(batch=0)) == _lib.ECCO_OK  # nothing to do
 
 
