@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
 //   O_i += P_i V_j    (P from TMEM, V as it lies: rows of keys, N-major)
 // With more than 128 rows ("wide") engine i has rows 128 i .. of every tile;
 // with fewer ("thin") both have the same rows, engine i the key tiles i, i + 2,
-// .. of the part, and engine 0 joins the two.  Warps 0-3 and 4-7 are the
+// .. of the part, and engine 0 joins the two; or two thin parts of as many tiles
+// have an engine each.  Warps 0-3 and 4-7 are the
 // engines' softmax, a thread a row = a TMEM lane; warp 8 issues the products,
 // warp 9 the copies (a tile is one 32 KB bulk copy), warp 10 works out the
 // share's parts and hands them to the others.
@@ -379,13 +380,15 @@ struct AttnArgs {
 constexpr int kRows = 256;               // rows of an item
 constexpr int kAttnThreads = 352;        // 8 softmax warps, products, copies, plan
 constexpr int kStages = 4;               // K and V tiles in flight
-constexpr int kParts = 4;                // parts planned ahead
+constexpr int kParts = 4;                // parts (or pairs) planned ahead
+constexpr int kPartBytes = 96;           // two of 48
+constexpr int kPairTiles = 8;            // the longest first part of a pair
 constexpr int kMaxCtas = 160;            // shares (and twice as many slots) at most
 constexpr int kBars = 2 * kStages + 2 * kParts + 13;
 constexpr size_t kOffRing = 2 * kTileBytes;
 constexpr size_t kOffBars = kOffRing + (size_t)kStages * kTileBytes;
 constexpr size_t kOffParts = kOffBars + (kBars * 8 + 8 + 15) / 16 * 16;  // the barriers, tensor-memory address, dead mark
-constexpr size_t kOffMl = kOffParts + kParts * 48;                       // engine 1's maxima and sums, for engine 0
+constexpr size_t kOffMl = kOffParts + kParts * kPartBytes;               // engine 1's maxima and sums, for engine 0
 constexpr size_t kOffSeq = kOffMl + 256 * sizeof(float);
 constexpr size_t kOffUnits = kOffSeq + 16 * ECCO_MAX_BATCH;
 constexpr size_t kOffTile = kOffUnits + 8 * (ECCO_MAX_BATCH + 1);
@@ -567,14 +570,22 @@ struct Plan {
 
 // One part of an item, as the planning warp hands it to the others: key tiles
 // [t0, t0 + n) of rows g0 .. g0 + rows - 1 (row = new token * group + query head
-// of the group).
+// of the group).  Two thin parts that follow one another and have as many tiles
+// (or the second one less) go as a pair, an engine each: the copies and products
+// are those of one thin part of the sum of their tiles.  Many short sequences of
+// 8 heads, us a call without pairs and with: 128 x 1 over up to 100 keys 73.8 and
+// 62.7, over 650 189 and 177.5, 64 x 4 over 200 65.2 and 54.8.  A part waits for
+// the next one to be planned only up to kPairTiles tiles (16: 75.8 us for 74.8 at
+// 16 x 1 over 2000, 73.6 without pairs), and never at a share's end.
 struct Part {
     int q0, base, keys, g0;  // the sequence's first token row, position of new token 0, keys; first row
-    int rows, t0, n, ends;   // rows = 0: no part follows; ends: 1 the item begins in this part, 2 it ends in it
+    int rows, t0, n, ends;   // rows = 0: no part follows; ends: 1 the item begins in this part, 2 it ends in it, 4 one of a pair
     int tile_k, tile_v, h;   // scratch tiles of key tile t0, head of the round
     __device__ __forceinline__ bool thin() const { return rows <= 128; }
+    __device__ __forceinline__ bool pair() const { return ends & 4; }
+    __device__ __forceinline__ bool split() const { return thin() && !pair(); }                  // its tiles on both engines
     __device__ __forceinline__ int row0(int i) const { return thin() ? 0 : 128 * i; }  // of engine i's tile
-    __device__ __forceinline__ int tiles(int i) const { return thin() ? (n + 1 - i) >> 1 : n; }
+    __device__ __forceinline__ int tiles(int i) const { return split() ? (n + 1 - i) >> 1 : n; }
 };
 
 // a / b, not negative: in 32 bits where both fit (a 64-bit division costs 500
@@ -644,20 +655,37 @@ __device__ void plan_parts(const AttnArgs& A, uint8_t* smem, uint32_t bar_part, 
     int4 cut = make_int4(0, -1, 0, 0);
     uint32_t slot = 0;
     bool ok = true;
-    auto hand = [&](const int4& a, const int4& b, const int4& c) {
-        const uint32_t i = slot % kParts, use = slot / kParts;
-        // (as long as the softmax works on the parts ahead, so with a limit of its
-        // own; it ends as well once any other wait of the CTA has given up)
-        if (use > 0 && ok) ok = mbar_wait(bar_taken + 8 * i, (use - 1) & 1, dead, A.flag, 1u << 30);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok && lane == 0) {
-            int4* d = reinterpret_cast<int4*>(smem + kOffParts + 48 * i);
-            d[0] = a;
-            d[1] = b;
-            d[2] = c;
-            mbar_arrive(bar_part + 8 * i);
+    // A part that was planned and not handed on yet: the next one may go with it.
+    int4 last[3]{make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+    bool waits = false;
+    // Hands on `x`, before it the part that waits (with x, if they are a pair), or
+    // lets x wait.  Out of line: the instructions of a call are fetched anew.
+    auto hand = [&](const int4 (&x)[3], bool pair, bool wait) {
+#pragma unroll 1
+        for (int k = waits ? 0 : 1; k < (pair || wait ? 1 : 2); ++k) {
+            const uint32_t i = slot % kParts, use = slot / kParts;
+            // (as long as the softmax works on the parts ahead, so with a limit of its
+            // own; it ends as well once any other wait of the CTA has given up)
+            if (use > 0 && ok) ok = mbar_wait(bar_taken + 8 * i, (use - 1) & 1, dead, A.flag, 1u << 30);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && lane < 3) {
+                int4* d = reinterpret_cast<int4*>(smem + kOffParts + kPartBytes * i);
+                int4 v = lane == 0 ? last[0] : lane == 1 ? last[1] : last[2], w = lane == 0 ? x[0] : lane == 1 ? x[1] : x[2];
+                if (k) v = w;
+                if (lane == 1 && pair) {
+                    v.w |= 4;
+                    w.w |= 4;
+                }
+                d[lane] = v;
+                if (pair) d[3 + lane] = w;
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(bar_part + 8 * i);
+            ++slot;
         }
-        ++slot;
+        waits = wait;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) last[k] = x[k];
     };
     if (total > 0 && blockIdx.x < shares) {
         const long long u0 = quotient(total * blockIdx.x, shares), stop = quotient(total * (blockIdx.x + 1), shares);
@@ -709,8 +737,12 @@ __device__ void plan_parts(const AttnArgs& A, uint8_t* smem, uint32_t bar_part, 
             if (until <= skip) break;
             const int begins = skip == 0, ends = until == units;
             const int tile = h * tiles + P.tile()[b] + r.t0 + skip;
-            hand(make_int4(s.q0, s.base, s.keys, qt * kRows), make_int4(r.rows, r.t0 + skip, min(until, r.n) - skip, begins | ends << 1),
-                 make_int4(tile, tile + A.hn * tiles, h, 0));
+            int4 part[3]{make_int4(s.q0, s.base, s.keys, qt * kRows),
+                         make_int4(r.rows, r.t0 + skip, min(until, r.n) - skip, begins | ends << 1),
+                         make_int4(tile, tile + A.hn * tiles, h, 0)};
+            const int n0 = last[1].z, n1 = part[1].z;
+            const bool pair = waits && r.rows <= 128 && n1 > 0 && (n0 == n1 || n0 == n1 + 1);
+            hand(part, pair, !pair && r.rows <= 128 && n1 > 0 && n1 <= kPairTiles && item + (long long)units * cost < stop);
             if (begins && !ends)
                 cut = make_int4(s.q0, h, qt * kRows, (int)quotient((item + (long long)units * cost) * shares - 1, total) | r.rows << 16);
             item += (long long)units * cost;
@@ -718,7 +750,8 @@ __device__ void plan_parts(const AttnArgs& A, uint8_t* smem, uint32_t bar_part, 
             ++qt;
         }
     }
-    hand(make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0));
+    const int4 end[3]{make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+    hand(end, false, false);
     launch_dependents();  // no earlier: the joining CTAs would sit on the SMs meanwhile
     if (lane == 0) A.part_item[blockIdx.x] = cut;
 }
@@ -757,14 +790,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
 
     bool ok = true;
     uint32_t taken = 0;
-    auto take = [&]() -> Part {  // the next part; rows = 0 after the last, or if the CTA gave up
-        const uint32_t i = taken % kParts;
-        if (ok) ok = mbar_wait(bar_part + 8 * i, (taken / kParts) & 1, dead, A.flag);
-        ++taken;
-        const int4* d = reinterpret_cast<const int4*>(smem + kOffParts + 48 * i);
+    auto read = [&](uint32_t i, int which) -> Part {
+        const int4* d = reinterpret_cast<const int4*>(smem + kOffParts + kPartBytes * i) + 3 * which;
         const int4 a = d[0], b = d[1], c = d[2];
         return Part{a.x, a.y, a.z, a.w, ok ? b.x : 0, b.y, b.z, b.w, c.x, c.y, c.z};
     };
+    // The next part, of a pair that of engine `engine`; rows = 0 after the last, or if
+    // the CTA gave up.
+    auto take = [&](int engine) -> Part {
+        const uint32_t i = taken % kParts;
+        if (ok) ok = mbar_wait(bar_part + 8 * i, (taken / kParts) & 1, dead, A.flag);
+        ++taken;
+        Part x = read(i, 0);
+        if (engine && x.pair()) x = read(i, 1);
+        return x;
+    };
+    auto other = [&]() -> Part { return read((taken - 1) % kParts, 1); };  // the pair's second, before it is given back
     auto give_back = [&]() { mbar_arrive(bar_taken + 8 * ((taken - 1) % kParts)); };  // one lane, once the part is in registers
 
     // The ring's tiles, in the order in which the products take them: wide parts
@@ -777,13 +818,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
             uint32_t n = 0;
             after_previous();  // the tiles are decoded
             for (;;) {
-                const Part x = take();
+                const Part x = take(0);
+                Part y{};
+                if (x.rows && x.pair()) y = other();
                 give_back();
                 if (!x.rows) break;
                 int k = 0, v = 0;
-                while (k + v < 2 * x.n) {
-                    const bool key = k < min(x.n, v + (x.thin() ? 2 : 1));
-                    const int64_t tile = key ? x.tile_k + k++ : x.tile_v + v++;
+                const int tiles = x.n + y.n;
+                while (k + v < 2 * tiles) {
+                    const bool key = k < min(tiles, v + (x.thin() ? 2 : 1));
+                    const int at = key ? k++ : v++;
+                    const Part& z = x.pair() && (at & 1) ? y : x;
+                    const int64_t tile = (key ? z.tile_k : z.tile_v) + (x.pair() ? at >> 1 : at);
                     const uint32_t st = n % kStages, use = n / kStages;
                     if (use > 0 && ok) ok = mbar_wait(bar_empty + 8 * st, (use - 1) & 1, dead, A.flag);
                     if (!ok) break;
@@ -810,20 +856,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
         auto wait = [&](uint32_t bar, uint32_t parity) { ok = mbar_wait(bar, parity & 1, dead, A.flag) && ok; };
         auto full = [&](uint32_t k) { wait(bar_full + 8 * (k % kStages), k / kStages); };  // ring tile k has landed
         for (;;) {
-            const Part x = take();
+            const Part x = take(0);
+            int n = x.n;
+            if (x.rows && x.pair()) n += other().n;
             ok = __all_sync(0xffffffffu, ok);
             if (lane == 0) give_back();
             if (!x.rows || !ok) break;
-            if (x.n == 0) continue;
+            if (n == 0) continue;
             const bool thin = x.thin();
-            const int steps = thin ? x.n : 2 * x.n;
+            const int steps = thin ? n : 2 * n;
             uint32_t v = 0, k = 0;  // ring tiles in use
             // step e: O_i += P_i times its values, then S_i of its engine's next keys (from step -2 on: S alone)
 #pragma unroll 1
             for (int e = -2; e < steps; ++e) {
                 const int i = e & 1;
                 const bool fresh = thin || i == 0, last = thin || i == 1;  // of the engines that share the tiles
-                const bool more = (thin ? e + 2 : (e >> 1) + 1) < x.n;
+                const bool more = (thin ? e + 2 : (e >> 1) + 1) < n;
                 if (fresh) {
                     if (e >= 0) full(v = at++);
                     if (more) full(k = at++);
@@ -880,7 +928,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
         // one pass more than parts: Q of the next part is loaded, and its first
         // products can start, before this one's output is written
         for (bool have = false;; have = true) {
-            Part y = take();
+            Part y = take(i);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) y.rows = 0;
             if (lane == 0) give_back();
@@ -903,7 +951,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
             if (have) {
                 // ---- part x is done: its rows of the output, or of the part's slot
                 const int r = x.row0(i) + row, g = x.g0 + r, n = x.tiles(i), tok = g / A.group;
-                const bool both = x.thin() && x.n > 1;  // a thin part on both engines
+                const bool both = x.split() && x.n > 1;  // a thin part on both engines
                 const bool real = r < x.rows, idle = x.row0(i) + (warp & 3) * 32 >= x.rows;
                 if (n > 0) wait(bar_o + 8 * i, no - 1);
                 if (both && i == 1) {  // O_1 stays in tensor memory until engine 0 has read it
@@ -912,7 +960,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                     tc_fence_before();
                     mbar_arrive(bar_x);
                     ++nx;
-                } else if (i == 0 || !x.thin()) {
+                } else if (i == 0 || !x.split()) {
                     float f0 = 1.0f, f1 = 0.0f;
                     if (both) {
                         wait(bar_x, nx++);
@@ -922,7 +970,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                         l = l * f0 + l1 * f1;
                         m = mn;
                     }
-                    const bool whole = x.ends == 3;
+                    const bool whole = (x.ends & 3) == 3;
                     const int64_t slot = 2 * (int64_t)blockIdx.x + (x.ends & 1);
                     const int qh = (A.h0 + x.h) * A.group + g - tok * A.group;
                     const int64_t at = (int64_t)x.q0 + tok;
@@ -977,7 +1025,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
             }
             if (!y.rows) break;
             x = y;
-            const int r = x.row0(i) + row, n = x.tiles(i), step = x.thin() ? 2 : 1;
+            const int r = x.row0(i) + row, n = x.tiles(i), step = x.split() ? 2 : 1;
             const Seq s{x.q0, 0, x.base, x.keys};
             const bool real = r < x.rows, idle = x.row0(i) + (warp & 3) * 32 >= x.rows;  // idle: no row of this warp is one
             const int tok = real ? (x.g0 + r) / A.group : 0;
@@ -991,7 +1039,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
             m = -INFINITY;
             l = 0.0f;
             for (int j = 0; j < n; ++j) {
-                const int k0 = (x.t0 + (x.thin() ? i : 0) + j * step) * kTile;
+                const int k0 = (x.t0 + (x.split() ? i : 0) + j * step) * kTile;
                 wait(bar_s + 8 * i, ns++);
                 if (j == 0 && i == 1 && nx > 0) wait(bar_x + 8, nx - 1);  // engine 0 has read the last thin part's O_1
                 if (idle) {  // its lanes of P are whatever they are: rows do not mix

@@ -301,6 +301,17 @@ def test_attention_few_rows(new, lens, H, G, page, window, scale, kk, vk, max_kv
     one_attention(new, lens, H, G, page, window, scale, "learned_kv", "random1", kk, vk, max_q=max(new), max_kv=max_kv)
 
 
+@pytest.mark.parametrize("most_new,most_kv,H,G,window", [(1, 128, 8, 4, 0), (1, 700, 5, 3, 0), (30, 300, 4, 4, 0), (2, 1500, 3, 2, 140)])
+def test_attention_many_short_sequences(most_new, most_kv, H, G, window):
+    """More items than CTAs, of one to a few tiles: runs of equal, shorter and longer ones, some with no row or no key."""
+    rng = np.random.default_rng(most_kv)
+    new = rng.integers(0, most_new + 1, 110)
+    new[new == 0] = rng.integers(0, 2, (new == 0).sum())
+    lens = rng.integers(0, most_kv + 1, 110)
+    lens[:40] = np.repeat(lens[:10], 4)  # neighbours of the same length
+    one_attention(new.tolist(), lens.tolist(), H, G, 64, window, 0.0884, "learned_kv", "random1", "kv", "kv", max_q=most_new)
+
+
 def test_attention_few_rows_bounds_garbage_and_bad_pages():
     kt, vt = table_set("learned_kv"), table_set("random1")
     rng = np.random.default_rng(9)
