@@ -1568,10 +1568,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) paged_small_kernel(const __g
     if (warp == 15) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(256u) : "memory");
 }
 
+// Scratch of one KV head.
+int64_t head_bytes(int batch, int max_kv) { return 2 * (int64_t)batch * ((max_kv + kTile - 1) / kTile) * kTileBytes; }
+
 // Heads of a round: as many as keep the scratch within kRoundBytes, at least one.
 int round_heads(int batch, int kv_heads, int max_kv)
 {
-    const int64_t per_head = 2 * (int64_t)batch * ((max_kv + kTile - 1) / kTile) * kTileBytes;
+    const int64_t per_head = head_bytes(batch, max_kv);
     return (int)std::max<int64_t>(1, std::min<int64_t>(kv_heads, per_head ? kRoundBytes / per_head : kv_heads));
 }
 
@@ -1589,8 +1592,10 @@ Layout layout(int batch, int kv_heads, int group, int max_q, int max_kv)
     L.ml = up(kMaxCtas * sizeof(int4));
     L.o = L.ml + up((size_t)2 * kMaxCtas * 2 * L.slot_rows * sizeof(float));
     L.scratch = L.o + up((size_t)2 * kMaxCtas * 32 * L.slot_rows * sizeof(float4));
-    const int64_t tiles = (int64_t)batch * ((max_kv + kTile - 1) / kTile);
-    L.bytes = L.scratch + (size_t)(2 * round_heads(batch, kv_heads, max_kv) * tiles * kTileBytes) + 1024;
+    // A round may leave part of kRoundBytes free, more or less of it as the bounds
+    // grow.  It is asked for all the same: the size never shrinks when a bound grows.
+    const int64_t per_head = head_bytes(batch, max_kv);
+    L.bytes = L.scratch + (size_t)std::max(per_head, std::min(kv_heads * per_head, kRoundBytes)) + 1024;
     return L;
 }
 

@@ -256,6 +256,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
 
 
 def paged_attention_workspace_bytes(batch: int, kv_heads: int, group: int, max_q: int, max_kv: int) -> int:
+    """Bytes of workspace of a paged_attention call.  It never shrinks when an
+    argument grows: a workspace of the largest bounds serves every smaller call."""
     return int(_lib.load().ecco_paged_attention_workspace_bytes(batch, kv_heads, group, max_q, max_kv))
 
 

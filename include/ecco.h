@@ -387,7 +387,9 @@ int ecco_paged_append(const ecco_tables* k_tables, const ecco_tables* v_tables, 
  *   group 1..16; batch * kv_heads * max_kv and tokens * kv_heads * group below 2^40;
  *   workspace   caller-owned device scratch, 16-byte aligned, of
  *               ecco_paged_attention_workspace_bytes(...) bytes; no initial
- *               contents are needed.  Two calls that share it must be ordered.
+ *               contents are needed.  The size never shrinks when an argument
+ *               grows, so one of the largest bounds serves every smaller call.
+ *               Two calls that share it must be ordered.
  * A sequence may share pages with others, and the pools may be one.
  * The blocks are decoded into the workspace (the KV heads in rounds of at most
  * 1 GiB, or one head) and read from there by the tensor-core kernel.  Sums run

@@ -472,6 +472,20 @@ def test_attention_in_rounds_of_heads():
     check_attention(out, lse, attend(f64(bits(q)), pool_decode(kt, kb), pool_decode(vt, vb), table, kvl, cu, 0.0884, 0))
 
 
+def test_attention_with_a_workspace_of_larger_bounds():
+    """A workspace sized once for the largest batch and length, at bounds below them."""
+    kt = vt = table_set("learned_kv")
+    H, G, page, lens, new = 8, 4, 64, [300, 1, 130], [70, 1, 2]
+    ws = torch.empty(ecco.paged_attention_workspace_bytes(3, H, G, 100, 100_000), dtype=torch.uint8, device=DEV)
+    table, kvl, cu = meta(lens, new, page, 12, seed=3)
+    kb, vb = fill_pool(kt, 12, H, page, "kv", 3), fill_pool(vt, 12, H, page, "kv", 4)
+    q = torch.randn(73, H * G, 128, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).to(DEV)
+    ref = attend(f64(bits(q)), pool_decode(kt, kb), pool_decode(vt, vb), table, kvl, cu, 0.0884, 0)
+    for max_kv in (1 << 16, 87_381, 90_000, 100_000, 1000, 300):  # 8 heads a round, then 7, then 6
+        out, lse = run_attention(kb, vb, kt, vt, q, table, kvl, cu, 0.0884, max_q=70, max_kv=max_kv, workspace=ws)
+        check_attention(out, lse, ref)
+
+
 def test_attention_empty_tables_and_pools():
     t = ecco.Tables(table_set("learned_kv"))
     q = torch.randn(3, 4, 128, device=DEV).to(torch.bfloat16)

@@ -254,6 +254,20 @@ def test_workspace_sizes(lib):
     assert size(1, 8, 4, 1, 0) > 0
 
 
+def test_workspace_sizes_never_shrink():
+    """One workspace, sized for the largest bounds, serves every smaller call."""
+    size = ecco.paged_attention_workspace_bytes
+    base = dict(batch=1, kv_heads=8, group=4, max_q=500, max_kv=262144)
+    steps = {"batch": range(1, 70), "kv_heads": range(1, 70), "group": range(1, 17), "max_q": range(0, 300),
+             "max_kv": [n for m in range(1, 4000, 7) for n in (128 * m, 128 * m + 1)]}
+    for at in (base, dict(base, batch=3, max_kv=50000), dict(base, batch=16, max_q=1, max_kv=16384), dict(base, kv_heads=3, max_q=1)):
+        for name, values in steps.items():
+            got = [size(**{**at, name: v}) for v in values]
+            assert all(0 < a <= b for a, b in zip(got, got[1:])), (at, name)
+    assert size(1, 8, 4, 500, 262144) <= size(1, 8, 4, 500, 300000)
+    assert size(16, 8, 4, 1, 16384) <= size(17, 8, 4, 1, 16384)
+
+
 @pytest.mark.parametrize("call", [
     lambda x: ecco.rope(x, x, x),
     lambda x: ecco.copy_pages(x, x, [0], [1]),
