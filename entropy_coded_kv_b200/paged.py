@@ -73,6 +73,14 @@ def _call(fn, device, *args):
         _lib.check(rc, fn)
 
 
+def _int32(v, name):
+    """v as an int that the C call takes whole (ctypes would keep its low 32 bits)."""
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"{name} = {v} does not fit 32 bits")
+    return v
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -258,7 +266,9 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
 def paged_attention_workspace_bytes(batch: int, kv_heads: int, group: int, max_q: int, max_kv: int) -> int:
     """Bytes of workspace of a paged_attention call.  It never shrinks when an
     argument grows: a workspace of the largest bounds serves every smaller call."""
-    return int(_lib.load().ecco_paged_attention_workspace_bytes(batch, kv_heads, group, max_q, max_kv))
+    return int(_lib.load().ecco_paged_attention_workspace_bytes(
+        _int32(batch, "batch"), _int32(kv_heads, "kv_heads"), _int32(group, "group"), _int32(max_q, "max_q"),
+        _int32(max_kv, "max_kv")))
 
 
 def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_tables, v_tables,
@@ -294,15 +304,16 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         _dense(lse, _F32, 2, "lse", dev)
         if lse.shape != (tokens, heads):
             raise ValueError("lse must be [tokens, kv_heads * group]")
-    max_q = tokens if max_q is None else int(max_q)
-    max_kv = p.max_pages * p.page_size if max_kv is None else int(max_kv)
+    max_q = tokens if max_q is None else _int32(max_q, "max_q")
+    max_kv = p.max_pages * p.page_size if max_kv is None else _int32(max_kv, "max_kv")
+    window = _int32(window, "window")
     if workspace is None:
         workspace = torch.empty(max(1, paged_attention_workspace_bytes(p.batch, kv_heads, group, max_q, max_kv)),
                                 dtype=_U8, device=q.device)
     else:
         _dense(workspace, _U8, 1, "workspace", dev)
     _call("ecco_paged_attention", dev, k_tables.handle, v_tables.handle, p, k_pages.data_ptr(), v_pages.data_ptr(),
-          q.data_ptr(), *_strides(q, shape, "q"), group, tokens, max_q, max_kv, int(window), float(scale), out.data_ptr(),
+          q.data_ptr(), *_strides(q, shape, "q"), group, tokens, max_q, max_kv, window, float(scale), out.data_ptr(),
           *_strides(out, shape, "out"), _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out
 

@@ -815,3 +815,18 @@ def test_refusals_of_one_array_twice_and_of_wide_steps():
     with pytest.raises(ValueError):
         cache.compact(seqs, torch.ones(len(seqs), 1, dtype=torch.bool, device=DEV))
     assert cache.extend(seqs[1:], [0] * _lib.MAX_BATCH).tokens == 0
+
+
+@pytest.mark.parametrize("name", ["max_q", "max_kv", "window"])
+def test_bounds_past_32_bits_are_refused(name):
+    """Not cut to their low 32 bits: a window of 2^32 + 5 is none of 5."""
+    t = ecco.Tables(table_set("learned_kv"))
+    kp = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, device=DEV)
+    q = torch.zeros(5, 8, 128, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    for value in (1 << 31, 1 << 32, (1 << 32) + 5, -(1 << 32) + 5):
+        for w in (None, ws):
+            with pytest.raises(ValueError):
+                ecco.paged_attention(q, kp, kp, t, t, i32([[0, 1]]), i32([20]), i32([0, 5]), 1.0, workspace=w, **{name: value})
+    for value in (20, 64, 1 << 20):
+        ecco.paged_attention(q, kp, kp, t, t, i32([[0, 1]]), i32([20]), i32([0, 5]), 1.0, **{name: value})

@@ -268,6 +268,16 @@ def test_workspace_sizes_never_shrink():
     assert size(16, 8, 4, 1, 16384) <= size(17, 8, 4, 1, 16384)
 
 
+@pytest.mark.parametrize("at", range(5))
+@pytest.mark.parametrize("value", [1 << 31, 1 << 32, (1 << 32) + 1, -(1 << 31) - 1, -(1 << 32) + 4])
+def test_workspace_sizes_of_numbers_past_32_bits_are_refused(at, value):
+    """ctypes would pass their low 32 bits: 2^32 + 1 as one."""
+    args = [1, 1, 1, 1, 1]
+    args[at] = value
+    with pytest.raises(ValueError):
+        ecco.paged_attention_workspace_bytes(*args)
+
+
 @pytest.mark.parametrize("call", [
     lambda x: ecco.rope(x, x, x),
     lambda x: ecco.copy_pages(x, x, [0], [1]),
