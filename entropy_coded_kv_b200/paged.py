@@ -21,7 +21,8 @@ GROUP, BLOCK_BYTES = 128, 64
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16, torch.float32: _lib.F32}
 _BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
 _CONTIGUOUS = torch.contiguous_format
-_get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# (a torch without CUDA lacks these two; it can import the package, and has no tensor to call with)
+_get_device, _get_stream = (getattr(torch._C, f, None) for f in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
 
 # A single token's call lasts a few microseconds on the GPU, so the checks come
 # twice: one expression that holds for every valid call, and, where it does not,

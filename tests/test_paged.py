@@ -4,7 +4,10 @@ from __future__ import annotations
 
 import ctypes
 import math
+import os
 import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -288,3 +291,21 @@ def test_host_tensors_are_refused(call):
         call(torch.zeros(2, 2, 2, 64, dtype=torch.uint8))
     with pytest.raises((TypeError, ValueError)):
         call(torch.zeros(2, 2, 64))
+
+
+def test_the_package_imports_on_a_torch_without_cuda(lib):
+    """Such a torch has none of _C's CUDA calls; the formats, the book of pages and the frequencies need no device."""
+    code = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_get")]:
+    delattr(torch._C, name)
+import entropy_coded_kv_b200 as ecco
+assert ecco.PageAllocator(2, 4).free_pages == 2 and len(ecco.rope_frequencies(64)[0]) == 32
+try:
+    ecco.copy_pages(torch.zeros(2, 1, 1, 64, dtype=torch.uint8), torch.zeros(2, 1, 1, 64, dtype=torch.uint8), [0], [1])
+except ValueError:
+    print("refused")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
