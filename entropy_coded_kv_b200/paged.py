@@ -264,9 +264,14 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
           _ptr(positions), _FLAGS[bool(interleaved)][bool(inverse)], _ptr(stats))
 
 
+_BOUNDS = ("batch up to 1024, 1 to 1024 KV heads, group 1 to 16, max_q up to 2^26, max_kv up to 2^30, "
+           "batch * ceil(max_kv / 128) up to 2^24")
+
+
 def paged_attention_workspace_bytes(batch: int, kv_heads: int, group: int, max_q: int, max_kv: int) -> int:
-    """Bytes of workspace of a paged_attention call.  It never shrinks when an
-    argument grows: a workspace of the largest bounds serves every smaller call."""
+    """Bytes of workspace of a paged_attention call; 0 for bounds that the call
+    refuses.  It never shrinks when an argument grows: a workspace of the largest
+    bounds serves every smaller call."""
     return int(_lib.load().ecco_paged_attention_workspace_bytes(
         _int32(batch, "batch"), _int32(kv_heads, "kv_heads"), _int32(group, "group"), _int32(max_q, "max_q"),
         _int32(max_kv, "max_kv")))
@@ -313,9 +318,18 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                                 dtype=_U8, device=q.device)
     else:
         _dense(workspace, _U8, 1, "workspace", dev)
-    _call("ecco_paged_attention", dev, k_tables.handle, v_tables.handle, p, k_pages.data_ptr(), v_pages.data_ptr(),
-          q.data_ptr(), *_strides(q, shape, "q"), group, tokens, max_q, max_kv, window, float(scale), out.data_ptr(),
-          *_strides(out, shape, "out"), _ptr(lse), workspace.data_ptr(), workspace.numel())
+    try:
+        _call("ecco_paged_attention", dev, k_tables.handle, v_tables.handle, p, k_pages.data_ptr(), v_pages.data_ptr(),
+              q.data_ptr(), *_strides(q, shape, "q"), group, tokens, max_q, max_kv, window, float(scale), out.data_ptr(),
+              *_strides(out, shape, "out"), _ptr(lse), workspace.data_ptr(), workspace.numel())
+    except _lib.EccoError as e:
+        if e.code == _lib.ECCO_ERR_ARG:  # the two refusals that say too little
+            need = paged_attention_workspace_bytes(p.batch, kv_heads, group, max_q, max_kv)
+            if not need:
+                raise _lib.EccoError(e.code, f"ecco_paged_attention ({_BOUNDS})") from None
+            if workspace.numel() < need:
+                raise _lib.EccoError(e.code, f"ecco_paged_attention (a workspace of {workspace.numel()} bytes for {need})") from None
+        raise
     return out
 
 

@@ -384,10 +384,12 @@ int ecco_paged_append(const ecco_tables* k_tables, const ecco_tables* v_tables, 
  *   max_q, max_kv  bounds of the new tokens and of the keys of a sequence;
  *               what lies past them (the last new tokens, the last keys) is
  *               not computed and not seen;
- *   group 1..16; batch * kv_heads * max_kv and tokens * kv_heads * group below 2^40;
+ *   group 1..16; max_q up to 2^26, max_kv up to 2^30, batch * ceil(max_kv / 128)
+ *               up to 2^24; tokens * kv_heads * group up to 2^40;
  *   workspace   caller-owned device scratch, 16-byte aligned, of
  *               ecco_paged_attention_workspace_bytes(...) bytes; no initial
- *               contents are needed.  The size never shrinks when an argument
+ *               contents are needed.  The function returns 0 for arguments
+ *               that the call refuses.  The size never shrinks when an argument
  *               grows, so one of the largest bounds serves every smaller call.
  *               Two calls that share it must be ordered.
  * A sequence may share pages with others, and the pools may be one.

@@ -830,3 +830,20 @@ def test_bounds_past_32_bits_are_refused(name):
                 ecco.paged_attention(q, kp, kp, t, t, i32([[0, 1]]), i32([20]), i32([0, 5]), 1.0, workspace=w, **{name: value})
     for value in (20, 64, 1 << 20):
         ecco.paged_attention(q, kp, kp, t, t, i32([[0, 1]]), i32([20]), i32([0, 5]), 1.0, **{name: value})
+
+
+def test_refused_bounds_are_named():
+    t = ecco.Tables(table_set("learned_kv"))
+    kp = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, device=DEV)
+    q = torch.zeros(5, 8, 128, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device=DEV)
+    rest = (kp, kp, t, t, i32([[0, 1]]), i32([20]), i32([0, 5]), 1.0)
+    for w in (None, ws):
+        for bad in (dict(max_q=(1 << 26) + 1), dict(max_kv=(1 << 30) + 1)):
+            with pytest.raises(ecco.EccoError, match="max_q up to 2.26") as e:
+                ecco.paged_attention(q, *rest, workspace=w, **bad)
+            assert e.value.code == _lib.ECCO_ERR_ARG
+    with pytest.raises(ecco.EccoError, match="workspace of 65536 bytes"):
+        ecco.paged_attention(q, *rest, workspace=ws)
+    with pytest.raises(ecco.EccoError, match="argument"):
+        ecco.paged_attention(q, *rest, window=-1)

@@ -16,6 +16,8 @@ import entropy_coded_kv_b200 as ecco
 from entropy_coded_kv_b200 import _lib
 from entropy_coded_kv_b200.build import build
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
 
 @pytest.fixture(scope="module")
 def lib():
@@ -271,6 +273,16 @@ def test_workspace_sizes_never_shrink():
     assert size(16, 8, 4, 1, 16384) <= size(17, 8, 4, 1, 16384)
 
 
+def test_workspace_bounds_are_the_ones_the_header_states():
+    """batch to 1024, group to 16, max_q to 2^26, max_kv to 2^30, batch * ceil(max_kv / 128) to 2^24, whatever the KV heads."""
+    size = ecco.paged_attention_workspace_bytes
+    for good, bad in (((1024, 1024, 1, 1, 1 << 21), (1024, 1, 1, 1, (1 << 21) + 1)), ((1, 1, 16, 1 << 26, 1), (1, 1, 16, (1 << 26) + 1, 1)),
+                      ((2, 1024, 16, 1, 1 << 30), (2, 1, 1, 1, (1 << 30) + 1)), ((1024, 1024, 16, 1, 1), (1025, 1, 1, 1, 1))):
+        assert size(*good) > 0 and size(*bad) == 0
+    src = open(os.path.join(ROOT, "include", "ecco.h")).read()
+    assert "max_q up to 2^26, max_kv up to 2^30, batch * ceil(max_kv / 128)\n *               up to 2^24" in src
+
+
 @pytest.mark.parametrize("at", range(5))
 @pytest.mark.parametrize("value", [1 << 31, 1 << 32, (1 << 32) + 1, -(1 << 31) - 1, -(1 << 32) + 4])
 def test_workspace_sizes_of_numbers_past_32_bits_are_refused(at, value):
@@ -306,6 +318,5 @@ try:
 except ValueError:
     print("refused")
 """
-    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
