@@ -35,6 +35,7 @@ EXPORTED = [
     "ecco_decode_attention_staged", "ecco_decode_attention_staged_workspace_bytes",
     "ecco_selftest_wait_timeout", "ecco_rope_table", "ecco_rope", "ecco_paged_append", "ecco_paged_attention",
     "ecco_paged_attention_workspace_bytes", "ecco_copy_pages", "ecco_compact_pages",
+    "ecco_selftest_paged_wait_timeout",
 ]
 
 
@@ -92,7 +93,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ecco_strerror.restype = ctypes.c_char_p
     L.ecco_abi_version.argtypes = []
     L.ecco_device_timeouts.argtypes = [ctypes.POINTER(ctypes.c_uint)]
-    L.ecco_selftest_wait_timeout.argtypes = [P]
+    L.ecco_selftest_wait_timeout.argtypes = L.ecco_selftest_paged_wait_timeout.argtypes = [P]
     L.ecco_decode_attention_workspace_bytes.argtypes = [I, I, I, I]
     L.ecco_decode_attention_static.argtypes = [P, P, P, P, I64, I, I, I, I, P, ctypes.c_float, P, P]
     L.ecco_decode_attention.argtypes = [P, P, P, P, I64, I, I, I, I, P, ctypes.c_float, P, P,

@@ -89,6 +89,7 @@ int* timeout_flag();
 bool timeout_raised();
 cudaError_t paged_timeouts(unsigned int* n);  // the paged attention's count, current device
 cudaError_t launch_wait_timeout_selftest(cudaStream_t s);
+cudaError_t launch_paged_wait_selftest(cudaStream_t s);
 // Activation format: 64-value groups (the descriptor counts 64-value groups).
 cudaError_t launch_encode_act(const ecco_tables* t, const uint16_t* x, const ecco_desc& d,
                               uint8_t* blocks, ecco_stats* stats, cudaStream_t s);

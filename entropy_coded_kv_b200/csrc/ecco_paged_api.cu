@@ -164,6 +164,11 @@ extern "C" int ecco_paged_attention(const ecco_tables* kt, const ecco_tables* vt
     return status(launch_paged_attention(a, ws, (cudaStream_t)stream));
 }
 
+extern "C" int ecco_selftest_paged_wait_timeout(void* stream)
+{
+    return status(launch_paged_wait_selftest((cudaStream_t)stream));
+}
+
 extern "C" int ecco_copy_pages(uint8_t* k, uint8_t* v, int64_t n_pages, int64_t page_bytes, const int32_t* src,
                                const int32_t* dst, int64_t n, void* stream)
 {

@@ -256,7 +256,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     int64_t i = lo + tid;
     const uint8_t* src = i < stop ? locate(i) : nullptr;
     uint32_t dead = 0u;
-    if (!mbar_wait(bar, 0u, &dead, A.flag)) return;  // no tables: nothing is decoded, and the flag says so
+    // The lanes trade values below: all of a warp go on, or none.
+    if (!__all_sync(0xffffffffu, mbar_wait(bar, 0u, &dead, A.flag))) {  // no tables: nothing is decoded, and the flag says so
+        dead = 0u;
+        mbar_wait(bar, 0u, &dead, nullptr);  // the copies have landed before the CTA ends
+        return;
+    }
     const float S_t = tb->S_t;
     for (; i < stop; i += per_round) {
         const int here = min((int)(hi - (i - (tid & 31))), per_round - (tid & ~31));  // rows of this warp in the round: even
@@ -1561,7 +1566,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) paged_small_kernel(const __g
     }
     if (tid == 0) {
         if (cluster == 1) A.part_item[cta] = live && tile == 0 && count > 1 ? make_int4(s.q0, h, 0, (cta + count - 1) | rows << 16) : make_int4(0, -1, 0, 0);
-        if (!live) mbar_wait(bar_tables, 0u, dead, A.flag);  // the copies have landed before the CTA ends
+        uint32_t zero = 0u;  // the copies have landed before the CTA ends (they have, where blocks were decoded)
+        if (!live || !ok) mbar_wait(bar_tables, 0u, &zero, live ? nullptr : A.flag);
     }
     __syncthreads();
     tc_fence_after();
@@ -1570,6 +1576,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) paged_small_kernel(const __g
 
 // Scratch of one KV head.
 int64_t head_bytes(int batch, int max_kv) { return 2 * (int64_t)batch * ((max_kv + kTile - 1) / kTile) * kTileBytes; }
+
+// Waits, as the kernels above do but for some milliseconds, for a barrier at
+// which nothing arrives.
+__global__ void paged_wait_selftest_kernel(int* flag)
+{
+    __shared__ __align__(8) uint64_t s_bar;
+    if (threadIdx.x == 0) {
+        uint32_t dead = 0u;
+        mbar_init(smem_u32(&s_bar), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        mbar_wait(smem_u32(&s_bar), 0u, &dead, flag, kSpinLimit >> 6);
+    }
+}
 
 // Heads of a round: as many as keep the scratch within kRoundBytes, at least one.
 int round_heads(int batch, int kv_heads, int max_kv)
@@ -1607,6 +1626,12 @@ size_t paged_attention_bytes(int batch, int kv_heads, int group, int max_q, int 
 }
 
 cudaError_t paged_timeouts(unsigned int* n) { return cudaMemcpyFromSymbol(n, g_timeouts, sizeof(*n)); }
+
+cudaError_t launch_paged_wait_selftest(cudaStream_t s)
+{
+    paged_wait_selftest_kernel<<<1, 32, 0, s>>>(timeout_flag());
+    return cudaGetLastError();
+}
 
 // Launches a kernel whose CTAs may start before the previous kernel has ended
 // (it waits with after_previous).

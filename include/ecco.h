@@ -458,14 +458,15 @@ int ecco_huffman_lengths(const double* weights, int n, int max_len, uint8_t* len
 
 /* Number of bounded device-side waits (tensor-core decode+GEMV pipeline, paged
  * attention) that gave up since the library was loaded on the current device; 0
- * in normal operation.  A CTA whose wait gives up stops issuing tensor-core work,
- * adds nothing to y (writes no more of the attention's out) and returns instead
- * of hanging, so that launch's result is incomplete.  Because launches are asynchronous, the failure is reported
- * like CUDA's own asynchronous errors: it raises a host-visible flag, and
- * every later ecco_decode_gemv call with batch > 4 and every later
- * ecco_paged_attention call returns ECCO_ERR_TIMEOUT
- * (enqueuing nothing) until this function is called, which reads the count
- * and clears the flag.  Blocking (reads device memory). */
+ * in normal operation.  A CTA whose wait gives up stops and returns instead of
+ * hanging.  In the GEMV it adds nothing more to y, so that launch's y is
+ * incomplete.  In the paged attention the kernels behind it go on: what that call
+ * wrote to out and lse is undefined, in every row (no other memory is touched).
+ * Because launches are asynchronous, the failure is reported like CUDA's own
+ * asynchronous errors: it raises a host-visible flag, and every later
+ * ecco_decode_gemv call with batch > 4 and every later ecco_paged_attention call
+ * returns ECCO_ERR_TIMEOUT (enqueuing nothing) until this function is called,
+ * which reads the count and clears the flag.  Blocking (reads device memory). */
 #define ECCO_ERR_TIMEOUT (-8) /* a bounded device wait gave up in an earlier launch */
 int ecco_device_timeouts(unsigned int* out);
 
@@ -474,6 +475,8 @@ int ecco_device_timeouts(unsigned int* out);
  * second), on an mbarrier that nothing completes, so the wait gives up,
  * counts itself and raises the flag.  Asynchronous on `stream`. */
 int ecco_selftest_wait_timeout(void* stream);
+/* The same with the paged attention's wait, for some milliseconds. */
+int ecco_selftest_paged_wait_timeout(void* stream);
 
 const char* ecco_strerror(int code);
 int ecco_abi_version(void);

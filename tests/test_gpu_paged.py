@@ -847,3 +847,29 @@ def test_refused_bounds_are_named():
         ecco.paged_attention(q, *rest, workspace=ws)
     with pytest.raises(ecco.EccoError, match="argument"):
         ecco.paged_attention(q, *rest, window=-1)
+
+
+def test_a_paged_wait_that_gives_up_is_counted_and_reported():
+    """The paged kernels' own wait, on a barrier at which nothing arrives: it
+    ends, the paged count goes up by one, and the attention refuses until the
+    count is read."""
+    import ctypes
+
+    lib = _lib.load()
+    n, m = ctypes.c_uint(), ctypes.c_uint()
+    assert lib.ecco_device_timeouts(ctypes.byref(n)) == _lib.ECCO_OK
+    t = ecco.Tables(table_set("learned_kv"))
+    kp = torch.zeros(1, 1, 16, 64, dtype=torch.uint8, device=DEV)
+    q = torch.zeros(1, 1, 128, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((1, 1), 7.0, device=DEV)
+    call = lambda: ecco.paged_attention(q, kp, kp, t, t, i32([[0]]), i32([1]), i32([0, 1]), 1.0, lse=lse)  # noqa: E731
+    assert lib.ecco_selftest_paged_wait_timeout(None) == _lib.ECCO_OK
+    torch.cuda.synchronize()
+    with pytest.raises(ecco.EccoError) as e:
+        call()
+    assert e.value.code == _lib.ECCO_ERR_TIMEOUT
+    torch.cuda.synchronize()
+    assert lse.item() == 7.0  # nothing was enqueued
+    assert lib.ecco_device_timeouts(ctypes.byref(m)) == _lib.ECCO_OK and m.value == n.value + 1
+    call()
+    assert lse.item() == 0.0  # one key of zeros
