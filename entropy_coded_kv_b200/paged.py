@@ -290,7 +290,9 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     sees the last `window` keys up to its own.  max_q and max_kv bound the new
     tokens and the keys of one sequence (by default all rows, and what a
     page_table row holds); they size the workspace
-    (paged_attention_workspace_bytes), which may be passed to reuse it."""
+    (paged_attention_workspace_bytes), which may be passed to reuse it, and they
+    choose kernels: the same call gives the same bits, other bounds or another
+    batch values within the same roundings."""
     dev = _tables_on(k_tables, v_tables)
     _on(q, _BF16, 3, "q", dev)
     p = _paged(k_pages, v_pages, page_table, kv_lens, cu_q, dev)

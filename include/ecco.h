@@ -394,9 +394,12 @@ int ecco_paged_append(const ecco_tables* k_tables, const ecco_tables* v_tables, 
  *               Two calls that share it must be ordered.
  * A sequence may share pages with others, and the pools may be one.
  * The blocks are decoded into the workspace (the KV heads in rounds of at most
- * 1 GiB, or one head) and read from there by the tensor-core kernel.  Sums run
- * in an order that depends on the lengths and the device alone: the same call
- * gives the same bits.  ECCO_ERR_TIMEOUT: see ecco_device_timeouts. */
+ * 1 GiB, or one head) and read from there by the tensor-core kernel.  The order
+ * of the sums, and when a sum is rescaled, follow from every argument (max_q,
+ * max_kv and window choose kernels and rounds too), the lengths and the device:
+ * the same call on the same contents gives the same bits, one with other bounds
+ * or other sequences in the batch only values within the same roundings.
+ * ECCO_ERR_TIMEOUT: see ecco_device_timeouts. */
 size_t ecco_paged_attention_workspace_bytes(int batch, int kv_heads, int group, int max_q, int max_kv);
 int ecco_paged_attention(const ecco_tables* k_tables, const ecco_tables* v_tables, ecco_paged paged,
                          const uint8_t* k_pages, const uint8_t* v_pages, const uint16_t* q_bf16,
