@@ -540,6 +540,7 @@ class PagedCache:
             cache.append(step, layer, k, v, rope=table)  # keys turned, keys and values encoded
             out = cache.attend(step, layer, q, scale)    # q turned by rope(q, table, step.positions)
         t = cache.fork(s)                                # shares the pages
+        cache.shrink(s, n)                               # drops the tokens from n on (a rejected draft)
         cache.compact([s], keep)                         # drops tokens
         cache.free(t)
 
@@ -562,7 +563,17 @@ class PagedCache:
         shape = (self.layers, n_pages, kv_heads, page_size, BLOCK_BYTES)
         self.k_pages = torch.empty(shape, dtype=_U8, device=self.device)
         self.v_pages = torch.empty(shape, dtype=_U8, device=self.device)
-        self._position: dict[int, int] = {}
+        # per sequence: its length after the last compaction, and the position of the token after it
+        self._base: dict[int, tuple[int, int]] = {}
+
+    def _next_position(self, seq: int) -> int:
+        """The position of the sequence's next token, from its length, whoever changed that."""
+        n, position = self._base[seq]
+        have = self.book.length(seq)
+        if have < n:  # shrunk into what was compacted: those positions are not known any more, and none is given twice
+            n = have
+            self._base[seq] = n, position
+        return position + have - n
 
     def _ints(self, v):
         return torch.tensor(v, dtype=_I32).to(self.device)
@@ -573,20 +584,26 @@ class PagedCache:
 
     def add(self) -> int:
         s = self.book.add()
-        self._position[s] = 0
+        self._base[s] = 0, 0
         return s
 
     def fork(self, seq: int) -> int:
         s = self.book.fork(seq)
-        self._position[s] = self._position[seq]
+        self._base[s] = self._base[seq]
         return s
 
     def free(self, seq: int) -> None:
         self.book.free(seq)
-        del self._position[seq]
+        del self._base[seq]
 
     def length(self, seq: int) -> int:
         return self.book.length(seq)
+
+    def shrink(self, seq: int, length: int) -> None:
+        """Drops the tokens from `length` on, and the pages that only they used.
+        The next `extend` gives their positions again."""
+        self.book.shrink(seq, length)
+        self._next_position(seq)
 
     def extend(self, seqs: list[int], new: list[int]) -> Step:
         """Pages for new[i] more tokens of each sequence (OutOfPages if there are
@@ -594,15 +611,13 @@ class PagedCache:
         calls.  Pages that are shared and about to be written are copied."""
         if len(seqs) > _lib.MAX_BATCH:
             raise ValueError(f"at most {_lib.MAX_BATCH} sequences a step")
+        first = [self._next_position(s) for s in seqs]
         copies = self.book.extend(seqs, new)
         if copies:
             n = self.book.n_pages
             src = [a + l * n for l in range(self.layers) for a, _ in copies]
             dst = [b + l * n for l in range(self.layers) for _, b in copies]
             copy_pages(self.k_pages.flatten(0, 1), self.v_pages.flatten(0, 1), src, dst)
-        first = [self._position[s] for s in seqs]
-        for s, n in zip(seqs, new):
-            self._position[s] += n
         lens, cu = [self.book.length(s) for s in seqs], [0]
         for n in new:
             cu.append(cu[-1] + n)
@@ -638,7 +653,7 @@ class PagedCache:
         returns them."""
         if len(seqs) > _lib.MAX_BATCH:
             raise ValueError(f"at most {_lib.MAX_BATCH} sequences a call")
-        lens = [self.book.length(s) for s in seqs]
+        lens, after = [self.book.length(s) for s in seqs], [self._next_position(s) for s in seqs]
         if keep.dim() != 2 or keep.shape[0] != len(seqs) or keep.shape[1] < max(lens, default=0):
             raise ValueError("keep must be [len(seqs), at least the longest length]")
         if not seqs:
@@ -654,4 +669,5 @@ class PagedCache:
             self.book.cancel(fresh)
             raise
         self.book.settle(seqs, fresh, lengths)
+        self._base.update(zip(seqs, zip(lengths, after)))
         return lengths

@@ -723,6 +723,49 @@ def test_cache_from_prompt_to_fork_to_compaction():
     step([d], [1])
 
 
+@pytest.mark.parametrize("through_the_book", [False, True])
+def test_cache_shrink_gives_positions_again(through_the_book):
+    """A draft's rejected tokens: the ones that follow take their places, positions and all, as if the draft had never been."""
+    H, G, page = 2, 4, 16
+    t = ecco.Tables(table_set("learned_kv"))
+    table = ecco.rope_table(64, 128)
+    qkv = torch.randn(50, (G + 2) * H, 128, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).to(DEV)
+
+    def step(cache, s, rows):
+        st = cache.extend([s], [len(rows)])
+        q, k, v = qkv[rows].split([G * H, H, H], 1)
+        cache.append(st, 0, k, v, rope=table)
+        return st.positions.tolist(), cache.attend(st, 0, ecco.rope(q, table, st.positions), 0.0884)
+
+    drafted, plain = ecco.PagedCache(8, page, H, t, t), ecco.PagedCache(8, page, H, t, t)
+    shrink = (lambda s, n: drafted.book.shrink(s, n)) if through_the_book else drafted.shrink
+    a, b = drafted.add(), plain.add()
+    step(drafted, a, list(range(30)))
+    step(plain, b, list(range(30)))
+    draft, _ = step(drafted, a, [30, 31, 32, 33, 34])
+    assert draft == [30, 31, 32, 33, 34]
+    fork = drafted.fork(a)                           # shares the draft; its own positions go on behind it
+    shrink(a, 32)
+    assert drafted.length(a) == 32 and drafted.length(fork) == 35
+    got, out = step(drafted, a, [40, 41])
+    step(plain, b, [30, 31])
+    want, ref = step(plain, b, [40, 41])
+    assert got == want == [32, 33] and torch.equal(out, ref)
+    assert step(drafted, fork, [42])[0] == [35]
+    # behind a compaction the positions go on from the last one given, and a draft's are given again
+    keep = torch.arange(64, device=DEV)[None] % 2 == 0
+    assert drafted.compact([a], keep) == [17]
+    assert step(drafted, a, [43, 44])[0] == [34, 35]
+    shrink(a, 18)
+    assert step(drafted, a, [45])[0] == [35]
+    shrink(a, 10)                                    # into the compacted tokens: none of their positions again
+    assert step(drafted, a, [46, 47])[0] == [34, 35]
+    shrink(a, 0)
+    assert step(drafted, a, [48])[0] == [34] and drafted.length(a) == 1
+    with pytest.raises(ValueError):
+        drafted.shrink(a, 2)
+
+
 @pytest.mark.parametrize("max_kv", [240, 1 << 14])
 def test_captured_step_replays_on_new_lengths_and_streams(max_kv):
     """Append and attention captured into a graph on a side stream; replays
