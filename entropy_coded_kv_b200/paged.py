@@ -169,7 +169,8 @@ def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, interlea
          inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
     """x [tokens, heads, dim] (bf16, fp16 or fp32) with the first rotary_dim
     values of each head turned by the angles of its row's position (int32
-    [tokens]): pairs (i, i + rotary_dim / 2), or (2 i, 2 i + 1) if interleaved.
+    [tokens]; one outside the table takes its nearest row): pairs (i, i +
+    rotary_dim / 2), or (2 i, 2 i + 1) if interleaved.
     inverse turns back, which is also the gradient of x from that of the
     result.  `out` may be x."""
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
@@ -241,7 +242,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     into their pages: row cu_q[b] + i goes to position kv_lens[b] - (cu_q[b + 1]
     - cu_q[b]) + i of sequence b (kv_lens counts the new tokens).  With `rope`
     (a rope_table of at most 128 values) the keys are turned first, by their own
-    positions or by `positions` (int32 [tokens])."""
+    positions or by `positions` (int32 [tokens]); one outside the table takes its
+    nearest row."""
     dev = _tables_on(k_tables, v_tables)
     _on(k, _BF16, 3, "k", dev)
     _on(v, _BF16, 3, "v", dev)
@@ -523,11 +525,12 @@ class PageAllocator:
 
 class Step:
     """One batch's view of the cache, on the device: page_table, kv_lens (the
-    new tokens among them), cu_q, and the bounds max_q and max_kv."""
+    new tokens among them), cu_q, positions; and on the host the number of new
+    tokens, the bounds max_q and max_kv, and the largest position (-1: none)."""
 
-    def __init__(self, page_table, kv_lens, cu_q, positions, tokens, max_q, max_kv):
+    def __init__(self, page_table, kv_lens, cu_q, positions, tokens, max_q, max_kv, max_position=-1):
         self.page_table, self.kv_lens, self.cu_q, self.positions = page_table, kv_lens, cu_q, positions
-        self.tokens, self.max_q, self.max_kv = tokens, max_q, max_kv
+        self.tokens, self.max_q, self.max_kv, self.max_position = tokens, max_q, max_kv, max_position
 
 
 class PagedCache:
@@ -623,13 +626,17 @@ class PagedCache:
             cu.append(cu[-1] + n)
         positions = [p + i for p, n in zip(first, new) for i in range(n)]
         return Step(self._table_of([self.book.pages(s) for s in seqs]), self._ints(lens), self._ints(cu),
-                    self._ints(positions), cu[-1], max(new, default=0), max(lens, default=0))
+                    self._ints(positions), cu[-1], max(new, default=0), max(lens, default=0), max(positions, default=-1))
 
     def append(self, step: Step, layer: int, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor | None = None,
                interleaved: bool = False, stats: torch.Tensor | None = None) -> None:
-        """Encodes the step's keys and values (bf16 [tokens, kv_heads, 128]) into the layer's pages."""
+        """Encodes the step's keys and values (bf16 [tokens, kv_heads, 128]) into
+        the layer's pages.  A rope_table that ends before the step's positions is
+        refused (by `rope` it is not: it gets the positions on the device)."""
         if k.shape[0] != step.tokens:
             raise ValueError("k and v must have a row for each new token of the step")
+        if rope is not None and step.max_position >= rope.shape[0]:
+            raise ValueError(f"position {step.max_position} is past the {rope.shape[0]} of the rope_table")
         paged_append(k, v, self.k_pages[layer], self.v_pages[layer], self.k_tables[layer], self.v_tables[layer],
                      step.page_table, step.kv_lens, step.cu_q, rope=rope,
                      positions=step.positions if rope is not None else None, interleaved=interleaved, stats=stats)

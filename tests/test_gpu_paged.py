@@ -766,6 +766,29 @@ def test_cache_shrink_gives_positions_again(through_the_book):
         drafted.shrink(a, 2)
 
 
+def test_cache_refuses_positions_past_the_rope_table():
+    """The cache knows the positions: a key past the table would be turned by its last row, like the one before it."""
+    t = ecco.Tables(table_set("learned_kv"))
+    cache = ecco.PagedCache(8, 16, 2, t, t)
+    table = ecco.rope_table(20, 128)
+    s, other = cache.add(), cache.add()
+    x = torch.randn(24, 2, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    st = cache.extend([s, other], [20, 4])           # 0 .. 19: the table's last row
+    assert st.max_position == 19
+    cache.append(st, 0, x, x, rope=table)
+    before = cache.k_pages.clone()
+    st = cache.extend([s, other], [1, 1])            # 20
+    with pytest.raises(ValueError, match="position 20"):
+        cache.append(st, 0, x[:2], x[:2], rope=table)
+    assert torch.equal(cache.k_pages, before)
+    cache.append(st, 0, x[:2], x[:2], rope=ecco.rope_table(21, 128))
+    cache.append(st, 0, x[:2], x[:2])
+    assert cache.extend([other], [1]).max_position == 5
+    none = cache.extend([s], [0])
+    assert none.max_position == -1
+    cache.append(none, 0, x[:0], x[:0], rope=table)
+
+
 @pytest.mark.parametrize("max_kv", [240, 1 << 14])
 def test_captured_step_replays_on_new_lengths_and_streams(max_kv):
     """Append and attention captured into a graph on a side stream; replays
