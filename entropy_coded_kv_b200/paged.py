@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import heapq
 import math
+from array import array
 
 import torch
 
@@ -578,12 +579,21 @@ class PagedCache:
             self._base[seq] = n, position
         return position + have - n
 
-    def _ints(self, v):
-        return torch.tensor(v, dtype=_I32).to(self.device)
+    def _on_device(self, *lists):
+        """Each list of ints as int32 on the device, in one copy that nothing waits
+        for: from pinned memory, which torch keeps until the copy has run."""
+        flat = array("i")
+        for v in lists:
+            flat.extend(v)
+        host = torch.empty(len(flat), dtype=_I32, pin_memory=True)
+        host.copy_(torch.frombuffer(flat, dtype=_I32))
+        return host.to(self.device, non_blocking=True).split([len(v) for v in lists])
 
-    def _table_of(self, lists):
-        width = max((len(p) for p in lists), default=0)
-        return self._ints([p + [-1] * (width - len(p)) for p in lists]).view(len(lists), width)
+    @staticmethod
+    def _table_of(pages):
+        """Page lists as the rows of a table, -1 behind their ends: (entries, width)."""
+        width = max((len(p) for p in pages), default=0)
+        return [e for p in pages for e in p + [-1] * (width - len(p))], width
 
     def add(self) -> int:
         s = self.book.add()
@@ -611,7 +621,12 @@ class PagedCache:
     def extend(self, seqs: list[int], new: list[int]) -> Step:
         """Pages for new[i] more tokens of each sequence (OutOfPages if there are
         too few, with nothing changed), and the batch's view for the layers'
-        calls.  Pages that are shared and about to be written are copied."""
+        calls.  Pages that are shared and about to be written are copied.  Waits
+        for nothing on the device; the view is new memory each step, written by a
+        copy from the host, so it cannot be captured into a graph (a captured step
+        takes its own arrays, into which the view is copied)."""
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("extend copies from the host: not while a graph is captured")
         if len(seqs) > _lib.MAX_BATCH:
             raise ValueError(f"at most {_lib.MAX_BATCH} sequences a step")
         first = [self._next_position(s) for s in seqs]
@@ -625,8 +640,10 @@ class PagedCache:
         for n in new:
             cu.append(cu[-1] + n)
         positions = [p + i for p, n in zip(first, new) for i in range(n)]
-        return Step(self._table_of([self.book.pages(s) for s in seqs]), self._ints(lens), self._ints(cu),
-                    self._ints(positions), cu[-1], max(new, default=0), max(lens, default=0), max(positions, default=-1))
+        entries, width = self._table_of([self.book.pages(s) for s in seqs])
+        table, kv_lens, cu_q, pos = self._on_device(entries, lens, cu, positions)
+        return Step(table.view(len(seqs), width), kv_lens, cu_q, pos, cu[-1], max(new, default=0),
+                    max(lens, default=0), max(positions, default=-1))
 
     def append(self, step: Step, layer: int, k: torch.Tensor, v: torch.Tensor, rope: torch.Tensor | None = None,
                interleaved: bool = False, stats: torch.Tensor | None = None) -> None:
@@ -667,8 +684,9 @@ class PagedCache:
             return []
         fresh = self.book.replace(seqs)
         try:
-            table, dst = self._table_of([self.book.pages(s) for s in seqs]), self._table_of(fresh)
-            kv_lens = self._ints(lens)
+            entries, width = self._table_of([self.book.pages(s) for s in seqs])
+            table, dst, kv_lens = self._on_device(entries, self._table_of(fresh)[0], lens)
+            table, dst = table.view(len(seqs), width), dst.view(len(seqs), width)
             for layer in range(self.layers):
                 new = compact_pages(self.k_pages[layer], self.v_pages[layer], table, kv_lens, keep, dst)
             lengths = new.tolist()

@@ -789,6 +789,40 @@ def test_cache_refuses_positions_past_the_rope_table():
     cache.append(none, 0, x[:0], x[:0], rope=table)
 
 
+def test_cache_extend_waits_for_nothing():
+    """A step is prepared while the device is still busy, the copies of forked pages included."""
+    t = ecco.Tables(table_set("learned_kv"))
+    cache = ecco.PagedCache(64, 16, 2, [t, t], [t, t])
+    a, b = cache.add(), cache.add()
+    cache.extend([a, b], [40, 3])
+    cache.k_pages.random_(0, 256)
+    cache.v_pages.random_(0, 256)
+    forks = [cache.fork(a) for _ in range(2)]
+    for fork, new in zip(forks, (1, 2)):             # the first one sets up whatever a first call sets up
+        pages = cache.book.pages(fork)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(400_000_000)               # about 0.2 s
+        busy = torch.cuda.Event()
+        busy.record()
+        st = cache.extend([b, fork], [5, new])
+        waited = busy.query()
+        torch.cuda.synchronize()
+    assert not waited
+    assert st.page_table.tolist() == [cache.book.pages(b) + [-1] * 2, cache.book.pages(fork)] and len(cache.book.pages(b)) == 1
+    assert st.kv_lens.tolist() == [13, 42] and st.cu_q.tolist() == [0, 5, 7] and st.positions.tolist() == [8, 9, 10, 11, 12, 40, 41]
+    assert cache.book.pages(fork)[:2] == pages[:2] and cache.book.pages(fork)[2] != pages[2]
+    for pool in (cache.k_pages, cache.v_pages):
+        assert torch.equal(pool[:, pages[2]], pool[:, cache.book.pages(fork)[2]])
+    before = cache.length(a), cache.book.free_pages
+    side = torch.cuda.Stream()
+    with pytest.raises(RuntimeError, match="captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            cache.extend([a], [100])
+    assert (cache.length(a), cache.book.free_pages) == before
+    none = cache.extend([], [])
+    assert none.page_table.shape == (0, 0) and none.cu_q.tolist() == [0] and none.positions.numel() == 0
+
+
 @pytest.mark.parametrize("max_kv", [240, 1 << 14])
 def test_captured_step_replays_on_new_lengths_and_streams(max_kv):
     """Append and attention captured into a graph on a side stream; replays
