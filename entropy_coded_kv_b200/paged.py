@@ -172,8 +172,15 @@ def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, interlea
     values of each head turned by the angles of its row's position (int32
     [tokens]; one outside the table takes its nearest row): pairs (i, i +
     rotary_dim / 2), or (2 i, 2 i + 1) if interleaved.
-    inverse turns back, which is also the gradient of x from that of the
-    result.  `out` may be x."""
+    inverse takes the angles' negatives, which is the gradient of x from that of
+    the result; it undoes a turn by a table of magnitude 1, one of magnitude m
+    (yarn) it returns times m * m.  `out` may be x.  The result of an x that
+    requires a gradient has one (not with `out`: torch would not know of the
+    write)."""
+    if isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("x requires a gradient: no `out`, or under torch.no_grad()")
+        return _Rope.apply(x, table, positions, bool(interleaved), bool(inverse))
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPES:
         raise TypeError("x must be a bf16, fp16 or fp32 tensor")
     dev, shape = x.get_device(), x.shape
@@ -199,6 +206,25 @@ def rope(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, interlea
     _call("ecco_rope", dev, x.data_ptr(), *_strides(x, shape, "x"), out.data_ptr(), *_strides(out, shape, "out"), _DTYPES[x.dtype],
           tokens, heads, dim, table.data_ptr(), n, rotary, positions.data_ptr(), _FLAGS[bool(interleaved)][bool(inverse)])
     return out
+
+
+class _Rope(torch.autograd.Function):
+    """rope where autograd records: a linear map, its gradient is the transposed one."""
+
+    @staticmethod
+    def forward(ctx, x, table, positions, interleaved, inverse):
+        ctx.save_for_backward(table, positions)
+        ctx.flags = interleaved, inverse
+        return rope(x, table, positions, interleaved, inverse)
+
+    @staticmethod
+    def backward(ctx, dy):
+        table, positions = ctx.saved_tensors
+        interleaved, inverse = ctx.flags
+        dy = dy.contiguous()  # of a sum, say, it has no strides
+        if dy.data_ptr() % 16:
+            dy = dy.clone()
+        return rope(dy, table, positions, interleaved, not inverse), None, None, None, None
 
 
 # ------------------------------------------------------------------ the paged cache
@@ -285,7 +311,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
                     max_q: int | None = None, max_kv: int | None = None, window: int = 0,
                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """Causal attention of new tokens, already appended, over the paged cache.
+    """Causal attention of new tokens, already appended, over the paged cache (no
+    gradient).
 
     q: bf16 [tokens, kv_heads * group, 128], rows cu_q[b] .. cu_q[b + 1] - 1 the
     last tokens of sequence b.  Returns bf16 of q's shape; `lse` (fp32 [tokens,

@@ -325,8 +325,9 @@ int ecco_rope_table(const double* inv_freq, int n_freq, double magnitude, int64_
  *   (a cos - b sin,  b cos + a sin),
  * every product and sum one fp32 rounding, the result rounded once to the
  * type.  The pairs are values (i, i + rotary_dim / 2), or with
- * ECCO_ROPE_INTERLEAVED (2 i, 2 i + 1); ECCO_ROPE_INVERSE turns back (-sin):
- * the transpose of the turn, so also the gradient of x from that of y.
+ * ECCO_ROPE_INTERLEAVED (2 i, 2 i + 1); ECCO_ROPE_INVERSE takes -sin for sin:
+ * the transpose of the turn, so the gradient of x from that of y.  It undoes a
+ * turn by a table of magnitude 1 (magnitude m: x times m * m).
  *   x, y       [tokens][heads][dim]; token and head strides in elements, the
  *              values of a head contiguous; y may be x itself (same strides),
  *              otherwise they may not overlap;

@@ -109,6 +109,67 @@ def test_rope_gradient(inter):
         assert abs((f(h) - f(-h)) / 16 - got[at]) <= 1408 * 10 * 2.0**-23
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("inv", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rope_records_its_gradient(inter, inv, dtype):
+    """Through autograd: the same bits as the call for the gradient, by the formula and by differences."""
+    g = torch.Generator().manual_seed(5)
+    wide = torch.randn(11, 3, 80, generator=g).to(dtype).to(DEV).requires_grad_()
+    dy = torch.randn(11, 2, 64, generator=g).to(dtype).to(DEV)
+    pos = torch.randint(0, 300, (11,), generator=g, dtype=torch.int32).to(DEV)
+    table = ecco.rope_table(300, 48, scaling={"kind": "yarn", "factor": 4, "original": 100})
+    x = wide[:, 1:, 8:72]
+    with torch.no_grad():
+        assert not ecco.rope(x, table, pos).requires_grad
+    y = ecco.rope(x, table, pos, interleaved=inter, inverse=inv)
+    assert torch.equal(y, ecco.rope(x.detach(), table, pos, interleaved=inter, inverse=inv))
+    (got,) = torch.autograd.grad(y, wide, dy, retain_graph=True)
+    want = torch.zeros_like(got)
+    want[:, 1:, 8:72] = ecco.rope(dy, table, pos, interleaved=inter, inverse=not inv)
+    assert torch.equal(got, want)
+    formula, size = rotate(dy.cpu().double().numpy(), table.cpu().numpy(), pos.cpu().numpy(), 48, inter, not inv)
+    half = torch.finfo(dtype).eps / 2 if dtype != torch.float32 else 0.0
+    assert (np.abs(got[:, 1:, 8:72].cpu().double().numpy() - formula) <= 2.0**-24 * 2.01 * size + half * 1.01 * np.abs(formula)).all()
+    if dtype == torch.float32:
+        f = lambda v: float((ecco.rope(v, table, pos, interleaved=inter, inverse=inv).double() * dy.double()).sum())  # noqa: E731
+        for at in ((0, 0, 0), (3, 1, 30), (10, 0, 47), (5, 1, 60)):
+            h = torch.zeros(11, 2, 64, device=DEV)
+            h[at] = 8.0  # linear: a large step loses nothing but roundings (at most 4 values of size 10 at 2^-23)
+            assert abs((f(h) - f(-h)) / 16 - float(got[:, 1:, 8:72][at])) <= 1408 * 10 * 2.0**-23
+    # gradients that are one value everywhere, or begin between two 16-byte pieces; and the gradient's gradient
+    ones = torch.ones_like(dy)
+    (got,) = torch.autograd.grad(y.sum(), wide, retain_graph=True)
+    assert torch.equal(got[:, 1:, 8:72], ecco.rope(ones, table, pos, interleaved=inter, inverse=not inv))
+    odd = torch.zeros(dy.numel() + 1, dtype=dtype, device=DEV)[1:].view(dy.shape)
+    odd.copy_(dy)
+    (got,) = torch.autograd.grad(y, wide, odd, retain_graph=True)
+    assert torch.equal(got, want)
+    w = dy.clone().requires_grad_()
+    (first,) = torch.autograd.grad(y, wide, w, create_graph=True)
+    (second,) = torch.autograd.grad(first[:, 1:, 8:72], w, ones)
+    assert torch.equal(second, ecco.rope(ones, table, pos, interleaved=inter, inverse=inv))
+    for out in (x, torch.empty_like(dy)):
+        with pytest.raises(ValueError):
+            ecco.rope(x, table, pos, out=out)
+    with torch.no_grad():
+        out = torch.empty_like(dy)
+        assert ecco.rope(x, table, pos, out=out) is out
+
+
+def test_rope_and_its_gradient_captured():
+    table, pos = ecco.rope_table(64, 64), torch.arange(9, dtype=torch.int32, device=DEV)
+    x = torch.randn(9, 2, 64, device=DEV, requires_grad=True)
+    dy = torch.randn(9, 2, 64, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        (dx,) = torch.autograd.grad(ecco.rope(x, table, pos), x, dy)
+    for seed in range(2):
+        dy.copy_(torch.randn(9, 2, 64, generator=torch.Generator().manual_seed(seed)))
+        graph.replay()
+        assert torch.equal(dx, ecco.rope(dy, table, pos, inverse=True))
+
+
 # ------------------------------------------------------------------ append
 def meta(lens, new, page_size, n_pages, seed, width=None):
     """(page_table, kv_lens, cu_q) with pages drawn at random, -1 past a sequence's pages."""
