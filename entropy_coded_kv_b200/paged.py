@@ -366,10 +366,16 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
 
 
 def _host_ids(ids, name):
-    t = torch.as_tensor(ids, dtype=_I32) if not isinstance(ids, torch.Tensor) else ids
-    if t.dtype is not _I32 or t.get_device() >= 0 or t.dim() != 1:
-        raise TypeError(f"{name} must be a list or a one-dimensional int32 CPU tensor")
-    return t if t.is_contiguous() else t.contiguous()
+    """Page numbers on the host as an int32 tensor; none is rounded or cut to 32 bits."""
+    if isinstance(ids, torch.Tensor):
+        if ids.dtype is not _I32 or ids.get_device() >= 0 or ids.dim() != 1:
+            raise TypeError(f"{name} must be a list or a one-dimensional int32 CPU tensor")
+        return ids if ids.is_contiguous() else ids.contiguous()
+    try:
+        flat = array("i", ids)
+    except OverflowError:
+        raise ValueError(f"{name} holds a number past 32 bits") from None
+    return torch.frombuffer(flat, dtype=_I32) if flat else torch.empty(0, dtype=_I32)
 
 
 def copy_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, src, dst) -> None:

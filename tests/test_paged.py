@@ -9,6 +9,7 @@ import random
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
 
@@ -291,6 +292,23 @@ def test_workspace_sizes_of_numbers_past_32_bits_are_refused(at, value):
     args[at] = value
     with pytest.raises(ValueError):
         ecco.paged_attention_workspace_bytes(*args)
+
+
+def test_page_numbers_are_taken_whole():
+    """Lists and arrays of ints; a fraction or a number past 32 bits is no page number."""
+    from entropy_coded_kv_b200.paged import _host_ids
+
+    for good in ([3, 0, 7], (3, 0, 7), np.array([3, 0, 7]), torch.tensor([3, 0, 7], dtype=torch.int32),
+                 torch.tensor([3, 9, 0, 9, 7, 9], dtype=torch.int32)[::2]):
+        t = _host_ids(good, "src")
+        assert t.dtype == torch.int32 and t.is_contiguous() and t.tolist() == [3, 0, 7]
+    assert _host_ids([], "src").tolist() == []
+    for bad in ([1.5], [1.0], np.array([1.0]), "1", ["1"], [[1]], torch.tensor([1]), torch.tensor([[1]], dtype=torch.int32), torch.tensor([1.0])):
+        with pytest.raises(TypeError):
+            _host_ids(bad, "src")
+    for bad in ([1 << 31], [0, (1 << 32) + 1], np.array([(1 << 32) + 1]), [-(1 << 31) - 1]):
+        with pytest.raises(ValueError):
+            _host_ids(bad, "src")
 
 
 @pytest.mark.parametrize("call", [
