@@ -329,7 +329,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     shape = q.shape
     tokens, heads, dim = shape
     kv_heads = p.kv_heads
-    if dim != GROUP or heads % kv_heads:
+    if dim != GROUP or not kv_heads or heads % kv_heads:
         raise ValueError("q must be [tokens, kv_heads * group, 128]")
     group = heads // kv_heads
     if out is None:

@@ -1034,3 +1034,20 @@ def test_a_paged_wait_that_gives_up_is_counted_and_reported():
     assert lib.ecco_device_timeouts(ctypes.byref(m)) == _lib.ECCO_OK and m.value == n.value + 1
     call()
     assert lse.item() == 0.0  # one key of zeros
+
+
+def test_pools_without_heads_are_refused():
+    t = ecco.Tables(table_set("learned_kv"))
+    kp = torch.zeros(4, 0, 16, 64, dtype=torch.uint8, device=DEV)
+    tb, lens, cu = i32([[0, 1]]), i32([20]), i32([0, 5])
+    with pytest.raises(ValueError):
+        ecco.paged_attention(torch.zeros(5, 8, 128, dtype=torch.bfloat16, device=DEV), kp, kp, t, t, tb, lens, cu, 1.0)
+    none = torch.zeros(5, 0, 128, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises((ValueError, ecco.EccoError)):
+        ecco.paged_attention(none, kp, kp, t, t, tb, lens, cu, 1.0)
+    with pytest.raises((ValueError, ecco.EccoError)):
+        ecco.paged_append(none, none, kp, kp.clone(), t, t, tb, lens, cu)
+    with pytest.raises((ValueError, ecco.EccoError)):
+        ecco.compact_pages(kp, kp.clone(), tb, lens, torch.ones(1, 32, dtype=torch.bool, device=DEV), tb)
+    with pytest.raises((ValueError, ecco.EccoError)):
+        ecco.rope(none, ecco.rope_table(4, 128), i32([0] * 5))
