@@ -373,6 +373,21 @@ def test_attention_many_short_sequences(most_new, most_kv, H, G, window):
     one_attention(new.tolist(), lens.tolist(), H, G, 64, window, 0.0884, "learned_kv", "random1", "kv", "kv", max_q=most_new)
 
 
+@pytest.mark.parametrize("new,lens,H,G,window", [([530], [700], 2, 16, 0), ([1100, 3], [1300, 90], 1, 16, 300), ([5, 600], [400, 600], 1, 16, 0)])
+def test_attention_many_items_of_a_sequence(new, lens, H, G, window):
+    """More than 32 items of 256 rows in a sequence, more than 64 too: a share's first item is searched 32 at a time, and
+    so are a sequence's units summed."""
+    assert max(new) * G > 32 * 256
+    one_attention(new, lens, H, G, 64, window, 0.0884, "learned_kv", "random1", "kv", "kv")
+
+
+@pytest.mark.parametrize("new,lens,H,G,window", [([1], [131072], 1, 4, 0), ([1, 2], [100_001, 50_000], 1, 2, 0), ([3], [131_000], 1, 4, 100_000),
+                                                 ([40], [70_000], 1, 4, 0)])
+def test_attention_over_a_long_context(new, lens, H, G, window):
+    """An item cut into tens of parts, all of them joined."""
+    one_attention(new, lens, H, G, 64, window, 0.0884, "learned_kv", "random1", "kv", "kv", max_q=max(new))
+
+
 def test_attention_few_rows_bounds_garbage_and_bad_pages():
     kt, vt = table_set("learned_kv"), table_set("random1")
     rng = np.random.default_rng(9)

@@ -158,6 +158,21 @@ def test_frequencies():
         ecco.rope_frequencies(64, 1.0)
 
 
+def test_yarn_on_its_ramp():
+    """Pinned by hand: 128 values, base 10000, a context of 4096 stretched 8 times.  The pair that turns t times has the
+    index 128 ln(4096 / (2 pi t)) / (2 ln 10000): 20.94 for 32 turns, 45.03 for one.  So the ramp goes from 20 to 46:
+    pair 33 is halfway, kept by 1/2 and stretched by 1/2: 1/2 + 1/16 of its frequency."""
+    base = ecco.rope_frequencies(128)[0]
+    f, m = ecco.rope_frequencies(128, 10000.0, {"kind": "yarn", "factor": 8, "original": 4096})
+    ratio = [x / y for x, y in zip(f, base)]
+    for i, want in ((0, 1.0), (20, 1.0), (21, 25 / 26 + 1 / 208), (33, 0.5625), (45, 1 / 26 + 25 / 208), (46, 0.125), (63, 0.125)):
+        assert math.isclose(ratio[i], want, rel_tol=1e-12), i
+    assert math.isclose(m, 1.2079441541679836, rel_tol=1e-14)  # 0.1 ln 8 + 1
+    # other bounds of the ramp: 16 turns 25.76, 2 turns 40.21: from 25 to 41, pair 33 halfway again
+    f, _ = ecco.rope_frequencies(128, 10000.0, {"kind": "yarn", "factor": 2, "original": 4096, "low": 2, "high": 16})
+    assert math.isclose(f[33] / base[33], 0.75, rel_tol=1e-12) and math.isclose(f[29] / base[29], 0.875, rel_tol=1e-12)
+
+
 # ------------------------------------------------------------------ refusals, no device
 def paged(**kw):
     f = dict(n_pages=8, page_size=16, kv_heads=2, batch=1, max_pages=4, table_stride=4, page_table=4096, kv_lens=4096,
