@@ -14,6 +14,11 @@
 // bit 512, so only chunks with less room count how many of their codewords
 // end at or before bit 512; symbols from the first one that does not are
 // reported as invalid (decoded as +0).
+//
+// The frame around the walk -- header, null blocks, outlier records -- stands in
+// each kernel that decodes (read_record's callers); ecco_paged_attention.cu has it
+// twice, and in its kernel for few rows the chunks too, in a form for few warps.
+// A change to the block format has all of them to change.
 #pragma once
 
 #include "ecco_internal.cuh"

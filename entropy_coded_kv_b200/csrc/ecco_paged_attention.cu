@@ -27,6 +27,10 @@ constexpr int kTile = 128;                     // tokens of a scratch tile
 // 128-byte swizzle that the tensor cores read, so a tile goes to shared memory
 // as one contiguous copy.
 constexpr int kTileBytes = kTile * kG * 2;
+// The scratch of a round of KV heads, or of one head where that is more (128
+// sequences of 131072 keys: 8.6 GB).  Rounds within 140 or 280 MB took 71.5 and
+// 70.4 us for 70.6 at 8 x 1 over up to 4096, 179 and 165 for 165.7 at 1 over
+// 60000; larger calls were not compared.
 constexpr int64_t kRoundBytes = (int64_t)1 << 30;
 
 // What the device-side arrays say of one sequence, bounded.
@@ -526,7 +530,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 }
 
 // The weights 2^(c s - mc) of 32 scores, packed as bf16 into w, their sum added
-// to `sum`.
+// to `sum`.  bf16, because the second product takes both operands in one type and
+// V~ is bf16 by its definition: fp16 would lose its range, and tf32 halves the
+// rate and doubles the tiles.  The sum is of the fp32 weights, which the lse needs.
+// A weight is off by half a step (2^-8) at most; the outputs are 1.04 to 1.29
+// times as far from 64 bits as the same sums with fp32 weights (relative norm
+// 1.6e-3, the output's own rounding, and up to 2.1e-3).
 __device__ __forceinline__ void weights(const uint32_t* v, uint64_t c2, uint64_t mc2, uint32_t* w, uint64_t (&sum)[2])
 {
 #pragma unroll
@@ -1079,9 +1088,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_attention_kernel(const 
                     tmem_wait_st();
                 }
                 // Two passes over the scores, 64 columns at a time in loops that stay
-                // loops, not one pass over 128 registers: every SM fetches the step's
-                // instructions anew in every call.  (1 over 650: 22.4 us, and 23.3 all
-                // unrolled; 32 at a time 4096 over 16384 takes 5% longer.)
+                // loops: every SM fetches the step's instructions anew in every call
+                // (8 x 1 over up to 4096, this kernel, when it was chosen: 34 us, and
+                // 41 in one pass over 128 registers with the masked tiles in a copy of
+                // their own).  4096 over 16384: 32 columns at a time take 5% longer;
+                // one pass with registers moved between the warpgroups took 4% less
+                // (864 us for 897), but 1 over 650 14% more, which has since had a
+                // kernel of its own: that variant is open.
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
                 for (int k = 0; k < 128; k += 64) {

@@ -2,8 +2,9 @@
 // bound by HBM.  On one B200: 6000 page pairs of 32 KB, K and V, in 127 us
 // (6.2 TB/s read and written, two launches); half of 3 x 100000 tokens of 8
 // heads kept in 71 us -- 4.3 TB/s of the blocks moved, 5.2 TB/s of DRAM
-// traffic, since every other 64-byte block is read at random and DRAM brings
-// 1.5 times the bytes (231 MB for 154).
+// traffic: 231 MB are read for the 154 MB kept, 3/4 of all blocks, which is what
+// a random half costs when memory is fetched 128 bytes (two tokens) at a time.
+// Loads that ask for 64 were not tried.
 #include <algorithm>
 
 #include "ecco_paged.cuh"

@@ -34,7 +34,9 @@ struct Vec8 {  // 8 values: 16 bytes of a 16-bit type, 32 of fp32
 };
 
 // x is read once and streams past L2, which y should find room in: 22 us for
-// [8191, 32, 128] bf16 against 28 with plain loads (6.1 and 4.9 TB/s).
+// [8191, 32, 128] bf16 against 28 with plain loads (6.1 and 4.9 TB/s).  Calls one
+// behind the other on arrays that L2 does not hold: bf16 and fp16 26.7 us (5.1
+// TB/s), fp32 51.2 us (5.3 TB/s), halves or adjacent pairs, all of a head or half.
 template <typename T>
 __device__ __forceinline__ Vec8<T> load8(const T* p)
 {

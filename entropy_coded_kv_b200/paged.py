@@ -322,7 +322,10 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     page_table row holds); they size the workspace
     (paged_attention_workspace_bytes), which may be passed to reuse it, and they
     choose kernels: the same call gives the same bits, other bounds or another
-    batch values within the same roundings."""
+    batch values within the same roundings.  Rows of no sequence (before cu_q[0],
+    behind cu_q[-1]) and new tokens past max_q are not written: in `out` and `lse`
+    they stay as they were, in a result of the call's own they are whatever its
+    memory held."""
     dev = _tables_on(k_tables, v_tables)
     _on(q, _BF16, 3, "q", dev)
     p = _paged(k_pages, v_pages, page_table, kv_lens, cu_q, dev)
@@ -657,7 +660,9 @@ class PagedCache:
         calls.  Pages that are shared and about to be written are copied.  Waits
         for nothing on the device; the view is new memory each step, written by a
         copy from the host, so it cannot be captured into a graph (a captured step
-        takes its own arrays, into which the view is copied)."""
+        takes its own arrays, into which the view is copied).  The table is laid
+        out on the host each time: 0.05 ms at 8 sequences of 64 pages, 2.5 ms at
+        128 of 512."""
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("extend copies from the host: not while a graph is captured")
         if len(seqs) > _lib.MAX_BATCH:
