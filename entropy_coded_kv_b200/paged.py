@@ -75,10 +75,13 @@ def _call(fn, device, *args):
         _lib.check(rc, fn)
 
 
+_2_31 = 1 << 31
+
+
 def _int32(v, name):
     """v as an int that the C call takes whole (ctypes would keep its low 32 bits)."""
     v = int(v)
-    if not -(1 << 31) <= v < 1 << 31:
+    if not -_2_31 <= v < _2_31:
         raise ValueError(f"{name} = {v} does not fit 32 bits")
     return v
 
@@ -345,9 +348,11 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         _dense(lse, _F32, 2, "lse", dev)
         if lse.shape != (tokens, heads):
             raise ValueError("lse must be [tokens, kv_heads * group]")
-    max_q = tokens if max_q is None else _int32(max_q, "max_q")
-    max_kv = p.max_pages * p.page_size if max_kv is None else _int32(max_kv, "max_kv")
-    window = _int32(window, "window")
+    max_q = tokens if max_q is None else int(max_q)
+    max_kv = p.max_pages * p.page_size if max_kv is None else int(max_kv)
+    window = int(window)
+    if not (-_2_31 <= max_q < _2_31 and -_2_31 <= max_kv < _2_31 and -_2_31 <= window < _2_31):
+        _int32(max_q, "max_q"), _int32(max_kv, "max_kv"), _int32(window, "window")
     if workspace is None:
         workspace = torch.empty(max(1, paged_attention_workspace_bytes(p.batch, kv_heads, group, max_q, max_kv)),
                                 dtype=_U8, device=q.device)
