@@ -842,6 +842,84 @@ def test_cache_shrink_gives_positions_again(through_the_book):
         drafted.shrink(a, 2)
 
 
+@pytest.mark.parametrize("page", [1, 7, 16])
+def test_cache_against_a_model_of_the_tokens(page):
+    """Random requests, drafts taken back among them; each sequence's pages hold
+    the blocks of its own tokens, turned by the positions that a model gives."""
+    rng = np.random.default_rng(page)
+    H, layers = 2, 2
+    t, u = ecco.Tables(table_set("learned_kv")), ecco.Tables(table_set("random1"))
+    cache = ecco.PagedCache(600 // page, page, H, [t, u], [u, t])
+    table = ecco.rope_table(2000, 64)
+    want, position, floor = {}, {}, {}               # blocks [layer][pool][tokens, H, 64]; next position; length and position after a compaction
+    grown = 0
+
+    def check(seq):
+        n, pages = cache.length(seq), i32(cache.book.pages(seq)).long()
+        assert n == want[seq][0][0].shape[0]
+        at = torch.arange(n, device=DEV)
+        for layer in range(layers):
+            for pool, blocks in zip((cache.k_pages, cache.v_pages), want[seq][layer]):
+                assert torch.equal(pool[layer][pages[at // page], :, at % page], blocks)
+
+    for _ in range(150):
+        op = rng.choice(["add", "extend", "extend", "extend", "fork", "free", "shrink", "compact"])
+        seqs = list(want)
+        if op == "add" and len(seqs) < 6:
+            s = cache.add()
+            want[s], position[s], floor[s] = [[torch.empty(0, H, 64, dtype=torch.uint8, device=DEV)] * 2] * layers, 0, (0, 0)
+        elif op == "extend" and seqs:
+            some = rng.permutation(seqs)[:rng.integers(1, 4)].tolist()
+            new = rng.integers(0, 2 * page + 3, len(some)).tolist()
+            try:
+                st = cache.extend(some, new)
+            except ecco.OutOfPages:
+                continue
+            assert st.positions.tolist() == [position[s] + i for s, n in zip(some, new) for i in range(n)]
+            for layer in range(layers):
+                k, v = (torch.randn(sum(new), H, 128, device=DEV).to(torch.bfloat16) for _ in range(2))
+                cache.append(st, layer, k, v, rope=table)
+                turned = ecco.rope(k, table, st.positions) if sum(new) else k
+                blocks = [ecco.encode(x.reshape(-1), tb).view(-1, H, 64) if sum(new) else torch.empty(0, H, 64, dtype=torch.uint8, device=DEV)
+                          for x, tb in ((turned, cache.k_tables[layer]), (v, cache.v_tables[layer]))]
+                at = 0
+                for s, n in zip(some, new):
+                    want[s] = [[torch.cat([w, b[at:at + n]]) for w, b in zip(old, blocks)] if i == layer else old for i, old in enumerate(want[s])]
+                    at += n
+            for s, n in zip(some, new):
+                position[s] += n
+            grown += 1
+        elif op == "fork" and seqs and len(seqs) < 6:
+            s = rng.choice(seqs).item()
+            f = cache.fork(s)
+            want[f], position[f], floor[f] = want[s], position[s], floor[s]
+        elif op == "free" and len(seqs) > 2:
+            s = rng.choice(seqs).item()
+            cache.free(s)
+            del want[s], position[s], floor[s]
+        elif op == "shrink" and seqs:
+            s = rng.choice(seqs).item()
+            n = int(rng.integers(0, cache.length(s) + 1))
+            (cache if rng.random() < 0.5 else cache.book).shrink(s, n)
+            kept, first = floor[s]
+            position[s] = first + max(0, n - kept)
+            floor[s] = min(n, kept), first
+            want[s] = [[x[:n] for x in layer] for layer in want[s]]
+        elif op == "compact" and seqs:
+            some = rng.permutation(seqs)[:rng.integers(1, 3)].tolist()
+            keep = torch.from_numpy(rng.random((len(some), 700)) < 0.6).to(DEV)
+            try:
+                lens = cache.compact(some, keep)
+            except ecco.OutOfPages:
+                continue
+            for s, row, n in zip(some, keep, lens):
+                want[s] = [[x[row[:x.shape[0]]] for x in layer] for layer in want[s]]
+                floor[s] = n, position[s]
+        for s in want:
+            check(s)
+    assert grown > 20
+
+
 def test_cache_refuses_positions_past_the_rope_table():
     """The cache knows the positions: a key past the table would be turned by its last row, like the one before it."""
     t = ecco.Tables(table_set("learned_kv"))
