@@ -375,6 +375,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
 
 def _host_ids(ids, name):
     """Page numbers on the host as an int32 tensor; none is rounded or cut to 32 bits."""
+    if str(getattr(ids, "dtype", None)) == "int32":  # a numpy array: as it is
+        ids = torch.as_tensor(ids)
     if isinstance(ids, torch.Tensor):
         if ids.dtype is not _I32 or ids.get_device() >= 0 or ids.dim() != 1:
             raise TypeError(f"{name} must be a list or a one-dimensional int32 CPU tensor")

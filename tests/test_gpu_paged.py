@@ -548,6 +548,19 @@ def test_attention_in_rounds_of_heads():
     check_attention(out, lse, attend(f64(bits(q)), pool_decode(kt, kb), pool_decode(vt, vb), table, kvl, cu, 0.0884, 0))
 
 
+def test_attention_in_rounds_of_one_head():
+    """Bounds at which one head's tiles take more than a round: the heads one by one, 2 GiB each."""
+    kt = vt = table_set("learned_kv")
+    H, G, page, lens, new = 3, 4, 64, [300, 1], [70, 1]
+    table, kvl, cu = meta(lens, new, page, 8, seed=3, width=1 << 14)
+    kb, vb = fill_pool(kt, 8, H, page, "kv", 3), fill_pool(vt, 8, H, page, "kv", 4)
+    q = torch.randn(71, H * G, 128, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).to(DEV)
+    size = ecco.paged_attention_workspace_bytes(2, H, G, 71, 2 * page << 14)
+    assert 2 << 30 < size < (2 << 30) + (1 << 26) and size == ecco.paged_attention_workspace_bytes(2, 1, G, 71, 2 * page << 14)
+    out, lse = run_attention(kb, vb, kt, vt, q, table, kvl, cu, 0.0884, max_kv=2 * page << 14)
+    check_attention(out, lse, attend(f64(bits(q)), pool_decode(kt, kb), pool_decode(vt, vb), table, kvl, cu, 0.0884, 0))
+
+
 def test_attention_with_a_workspace_of_larger_bounds():
     """A workspace sized once for the largest batch and length, at bounds below them."""
     kt = vt = table_set("learned_kv")

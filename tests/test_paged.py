@@ -318,6 +318,10 @@ def test_page_numbers_are_taken_whole():
         t = _host_ids(good, "src")
         assert t.dtype == torch.int32 and t.is_contiguous() and t.tolist() == [3, 0, 7]
     assert _host_ids([], "src").tolist() == []
+    whole = np.arange(5, dtype=np.int32)
+    assert _host_ids(whole, "src").data_ptr() == whole.ctypes.data and _host_ids(whole[::2], "src").tolist() == [0, 2, 4]
+    with pytest.raises(TypeError):
+        _host_ids(whole[:4].reshape(2, 2), "src")
     for bad in ([1.5], [1.0], np.array([1.0]), "1", ["1"], [[1]], torch.tensor([1]), torch.tensor([[1]], dtype=torch.int32), torch.tensor([1.0])):
         with pytest.raises(TypeError):
             _host_ids(bad, "src")
